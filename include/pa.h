@@ -186,6 +186,69 @@ PA_API pa_status pa_decode_static_workspace(void* out, const void* q, const void
                                             int max_context_len, float scale, int partition_size,
                                             pa_dtype dtype, void* stream);
 
+/* ------------------------------------------------------------------ scores and eviction */
+
+/*
+ * Bytes of device workspace pa_decode_scores needs: pa_decode's, and 4 bytes per
+ * (sequence, query head, token of max_context_len) for the step's logits.  0 on
+ * invalid arguments.
+ */
+PA_API size_t pa_decode_scores_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                              int block_size, int max_context_len, int partition_size);
+
+/*
+ * pa_decode that also adds up how much each cached token is attended to.  out is
+ * pa_decode's; with w_i(h) the softmax weight of token i for query head h,
+ *   scores[s][kvh][i] += sum over the query heads h of kvh of w_i(h)   for i < context_lens[s] - 1,
+ *   scores[s][kvh][context_lens[s] - 1] = that sum                     (the token this step appended,
+ * which has no history: its entry needs no initial value, whatever an earlier token left there).
+ * Call it once per appended token.  Weights and sums are fp32, the heads added in order, so the
+ * same inputs give the same bits.
+ *   scores        [num_seqs][num_kv_heads][score_stride] fp32 (device, updated); entries from
+ *                 context_lens[s] on are untouched.  score_stride >= max_context_len
+ * Other arguments, checks and workspace rules as for pa_decode.
+ */
+PA_API pa_status pa_decode_scores(void* out, float* scores, const void* q, const void* k_cache, const void* v_cache,
+                                  const int32_t* block_tables, const int32_t* context_lens, int num_seqs,
+                                  int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                  int max_blocks_per_seq, int num_blocks, int max_context_len, int score_stride,
+                                  float scale, int partition_size, void* workspace, size_t workspace_bytes,
+                                  pa_dtype dtype, void* stream);
+
+/* Bytes of device workspace pa_evict needs.  0 on invalid arguments. */
+PA_API size_t pa_evict_workspace_size(int num_seqs, int num_kv_heads, int max_context_len);
+
+/*
+ * Eviction by accumulated attention weight.  Each kv head of sequence s keeps
+ * n = min(keep_lens[s], context_lens[s]) of its cached tokens: the recent ones (position
+ * greater than the head's largest position - min(num_recent, n)), then those of the largest
+ * score; among equal ones the lowest slot stays.  (A NaN ranks above +inf, -0 as +0.)
+ * Afterwards the head's first n slots hold the kept tokens: one before slot n stays where
+ * it is, and the r-th kept token from slot n on moves to the r-th gap, K and V rows, score
+ * and position alike.  The order of cached tokens changes; attention does not depend on it.
+ * Slots from n on keep their K and V rows.  The caller shortens the sequence
+ * (pa_alloc_truncate) and its context length to n.
+ *   k_cache/v_cache  pools (device, updated).  The blocks of slots < n of a sequence may be
+ *                    neither shared with another sequence nor cached (pa_alloc_make_private)
+ *   new_scores, new_positions  [num_seqs][num_kv_heads][score_stride] fp32 / int32 (device):
+ *                    entries below n are written, the others untouched.  They may be
+ *                    scores and positions themselves, but may not overlap them otherwise
+ *   scores, positions  the same shape (device): per slot, the accumulated weight
+ *                    (pa_decode_scores) and the token's position, distinct within a head
+ *   context_lens, keep_lens  [num_seqs] int32 (device).  A sequence with a negative one, or
+ *                    a context past max_context_len or its table row, raises
+ *                    PA_DEV_BAD_CONTEXT and is left as it is
+ *   max_context_len  host-side upper bound, at most 262144 (else PA_ERR_UNSUPPORTED) and
+ *                    at most score_stride
+ *   workspace        device scratch of pa_evict_workspace_size() bytes, 16-byte aligned;
+ *                    no initial contents.  Calls that share it must be ordered on one stream
+ */
+PA_API pa_status pa_evict(void* k_cache, void* v_cache, float* new_scores, int32_t* new_positions, const float* scores,
+                          const int32_t* positions, const int32_t* block_tables, const int32_t* context_lens,
+                          const int32_t* keep_lens, int num_recent, int num_seqs, int num_kv_heads, int head_dim,
+                          int block_size, int max_blocks_per_seq, int num_blocks, int max_context_len,
+                          int score_stride, void* workspace, size_t workspace_bytes, pa_dtype dtype, void* stream);
+
 /* ------------------------------------------------------------------ KV append */
 
 /*
@@ -414,6 +477,25 @@ PA_API pa_status pa_alloc_append_slots(pa_allocator* a, const int64_t* seq_ids, 
 PA_API pa_status pa_alloc_beam_step(pa_allocator* a, const int64_t* beam_ids, int num_beams, const int32_t* parents,
                                     const int64_t* new_ids, int num_new, int64_t* slots_out, int64_t* cow_pairs_out,
                                     int* num_cow_out);
+
+/*
+ * Copy-on-write ahead of a change to the first num_tokens tokens of a resident sequence
+ * (pa_evict writes into them): every block of theirs that another sequence shares or that
+ * the prefix cache holds is replaced by a fresh one, in table order, as an append would.
+ * (src, dst) pairs go to pairs_out[2 * n] (room for ceil(num_tokens / B) pairs) and
+ * *num_pairs_out = n; run one pa_copy_blocks on them first.  num_tokens is at most the
+ * sequence's.  Out of blocks: PA_ERR_OOM, nothing changes.
+ */
+PA_API pa_status pa_alloc_make_private(pa_allocator* a, int64_t seq_id, int num_tokens, int64_t* pairs_out,
+                                       int* num_pairs_out);
+
+/*
+ * Shortens a resident sequence to its first num_tokens tokens (at most its count): the
+ * blocks behind them lose its reference, in table order, as in pa_alloc_free_seq.
+ * PA_ERR_INVALID if that would end inside a block of the prefix cache, which a later append
+ * would then write into: make the sequence's tokens private first.
+ */
+PA_API pa_status pa_alloc_truncate(pa_allocator* a, int64_t seq_id, int num_tokens);
 
 /* Drops one reference to each block of seq_id; blocks reaching zero rejoin the free
  * pool, or stay in the prefix tree as unreferenced cached blocks. */

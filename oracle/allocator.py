@@ -233,6 +233,37 @@ class OracleAllocator:
         self.__dict__.update(trial.__dict__)
         return res
 
+    def make_private(self, seq_id, num_tokens):
+        """Fresh blocks in place of the shared or cached ones among the first num_tokens tokens' blocks;
+        returns [(src, dst)] in table order.  The sources are released after every block is taken."""
+        if seq_id not in self.tables or seq_id in self.on_host or not 0 <= num_tokens <= self.ntokens[seq_id]:
+            raise ValueError("unknown or swapped-out sequence, or too many tokens")
+        table = self.tables[seq_id]
+        at = [i for i in range(-(-num_tokens // self.B)) if self.ref[table[i]] > 1 or table[i] in self.key_of]
+        if len(at) > self.available():
+            raise OutOfBlocks()
+        pairs = [(table[i], self._take()) for i in at]
+        for i, (src, dst) in zip(at, pairs):
+            table[i] = dst
+        for src, _ in pairs:
+            self._release(src)
+        self.cow_count += len(pairs)
+        return pairs
+
+    def truncate(self, seq_id, num_tokens):
+        """Keeps the first num_tokens tokens; the blocks behind them are released in table order.  A block of
+        the prefix cache may not become the partial last one."""
+        if seq_id not in self.tables or seq_id in self.on_host or not 0 <= num_tokens <= self.ntokens[seq_id]:
+            raise ValueError("unknown or swapped-out sequence, or too many tokens")
+        n = -(-num_tokens // self.B)
+        table = self.tables[seq_id]
+        if num_tokens % self.B and table[n - 1] in self.key_of:
+            raise ValueError("the last block would be a partial one of the prefix cache")
+        for blk in table[n:]:
+            self._release(blk)
+        del table[n:]
+        self.ntokens[seq_id] = num_tokens
+
     def free_seq(self, seq_id):
         if seq_id not in self.tables:
             raise ValueError("unknown sequence")

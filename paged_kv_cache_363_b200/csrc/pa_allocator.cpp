@@ -519,6 +519,62 @@ pa_status pa_alloc_beam_step(pa_allocator* a, const int64_t* beam_ids, int num_b
     return PA_OK;
 }
 
+pa_status pa_alloc_make_private(pa_allocator* a, int64_t seq_id, int num_tokens, int64_t* pairs_out,
+                                int* num_pairs_out)
+{
+    if (!a || num_tokens < 0 || !num_pairs_out || (num_tokens > 0 && !pairs_out)) {
+        pa::set_error("pa_alloc_make_private: bad argument");
+        return PA_ERR_INVALID;
+    }
+    pa_allocator::Seq* q = a->resident(seq_id);
+    if (!q || num_tokens > q->tokens) {
+        pa::set_error("pa_alloc_make_private: unknown or swapped-out sequence, or more tokens than it has");
+        return PA_ERR_INVALID;
+    }
+    const size_t nblk = ((size_t)num_tokens + a->block_size - 1) / a->block_size;
+    auto shared = [a](int32_t b) { return a->ref[(size_t)b] > 1 || a->cached(b); };
+    int64_t need = 0;
+    for (size_t i = 0; i < nblk; ++i) need += shared(q->table[i]) ? 1 : 0;
+    if (need > a->available()) {
+        pa::set_error("pa_alloc_make_private: out of blocks");
+        return PA_ERR_OOM;
+    }
+    // every fresh block is taken before a source is released: an eviction may not hand out a
+    // source, which would then be read and written by one batch of copies
+    int n = 0;
+    for (size_t i = 0; i < nblk; ++i) {
+        const int32_t src = q->table[i];
+        if (!shared(src)) continue;
+        q->table[i] = a->take();
+        pairs_out[2 * n] = src;
+        pairs_out[2 * n + 1] = q->table[i];
+        ++n;
+    }
+    for (int k = 0; k < n; ++k) a->drop_ref((int32_t)pairs_out[2 * k]);
+    a->cow_copies += n;
+    *num_pairs_out = n;
+    return PA_OK;
+}
+
+pa_status pa_alloc_truncate(pa_allocator* a, int64_t seq_id, int num_tokens)
+{
+    pa_allocator::Seq* q = a && num_tokens >= 0 ? a->resident(seq_id) : nullptr;
+    if (!q || num_tokens > q->tokens) {
+        pa::set_error("pa_alloc_truncate: unknown or swapped-out sequence, or more tokens than it has");
+        return PA_ERR_INVALID;
+    }
+    const size_t nblk = ((size_t)num_tokens + a->block_size - 1) / a->block_size;
+    if (num_tokens % a->block_size != 0 && a->cached(q->table[nblk - 1])) {
+        pa::set_error("pa_alloc_truncate: the last block would be a partial one of the prefix cache "
+                      "(pa_alloc_make_private first)");
+        return PA_ERR_INVALID;
+    }
+    for (size_t i = nblk; i < q->table.size(); ++i) a->drop_ref(q->table[i]);
+    q->table.resize(nblk);
+    q->tokens = num_tokens;
+    return PA_OK;
+}
+
 pa_status pa_alloc_free_seq(pa_allocator* a, int64_t seq_id)
 {
     if (!a) return PA_ERR_INVALID;

@@ -157,47 +157,56 @@ pa_status decode_call(const char* fn, int phases, void* out, const void* q, cons
                       const void* v_cache, const int32_t* block_tables, const int32_t* context_lens, int num_seqs,
                       int num_heads, int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
                       int num_blocks, int max_context_len, float scale, int partition_size, void* workspace,
-                      size_t workspace_bytes, pa_dtype dtype, void* stream)
+                      size_t workspace_bytes, pa_dtype dtype, void* stream, bool with_scores = false,
+                      float* scores = nullptr, int score_stride = 0)
 {
-    const std::string name(fn);
+    const char* const name = fn;
+    auto set_error = [name](const std::string& msg) { pa::set_error(std::string(name) + msg); };
     pa_status st = check_common(fn, num_kv_heads, head_dim, block_size, num_blocks, dtype);
     if (st != PA_OK) return st;
     if (num_seqs < 0 || num_seqs > 65535 || num_heads <= 0 || max_blocks_per_seq <= 0 || max_context_len < 0 ||
         partition_size < 0 || !std::isfinite(scale)) {
-        set_error(name + ": bad size or scale");
+        set_error(": bad size or scale");
         return PA_ERR_INVALID;
     }
     if (num_heads % num_kv_heads != 0) {
-        set_error(name + ": num_heads must be a multiple of num_kv_heads");
+        set_error(": num_heads must be a multiple of num_kv_heads");
         return PA_ERR_INVALID;
     }
     const int group = num_heads / num_kv_heads;
     if (group != 1 && group != 2 && group != 4 && group != 8) {
-        set_error(name + ": num_heads / num_kv_heads must be 1, 2, 4 or 8");
+        set_error(": num_heads / num_kv_heads must be 1, 2, 4 or 8");
         return PA_ERR_UNSUPPORTED;
+    }
+    if (with_scores && score_stride < max_context_len) {
+        set_error(": score_stride must be at least max_context_len");
+        return PA_ERR_INVALID;
     }
     if (num_seqs == 0) return PA_OK;
     const bool run = (phases & kDecodeRun) != 0;
-    if ((run && (!out || !q || !k_cache || !v_cache)) || !block_tables || !context_lens) {
-        set_error(name + ": null pointer");
+    if ((run && (!out || !q || !k_cache || !v_cache)) || (with_scores && !scores) || !block_tables || !context_lens) {
+        set_error(": null pointer");
         return PA_ERR_INVALID;
     }
     if ((run && (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16))) ||
-        !aligned(block_tables, 4) || !aligned(context_lens, 4)) {
-        set_error(name + ": misaligned pointer (q, out, caches need 16 bytes)");
+        !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(scores, 4)) {
+        set_error(": misaligned pointer (q, out, caches need 16 bytes)");
         return PA_ERR_INVALID;
     }
     if (decode_uses_tensor_cores(dtype, head_dim, group) &&
         (int64_t)num_blocks * num_kv_heads * block_size > (int64_t)INT32_MAX) {
-        set_error(name + ": num_blocks * num_kv_heads * block_size must stay below 2^31 (tensor-copy row index)");
+        set_error(": num_blocks * num_kv_heads * block_size must stay below 2^31 (tensor-copy row index)");
         return PA_ERR_UNSUPPORTED;
     }
     const int p = resolve_partition(block_size, max_context_len, partition_size);
     if (p < 0) return (pa_status)p;
     const int np = max_context_len > 0 ? (max_context_len + p - 1) / p : 1;
-    const DecodeWorkspace wl = decode_workspace((size_t)num_seqs, (size_t)num_heads, (size_t)head_dim, (size_t)np);
-    if (!workspace || workspace_bytes < wl.total || !aligned(workspace, 16)) {
-        set_error(name + ": workspace missing, too small (need " + std::to_string(wl.total) +
+    const ScoresWorkspace sl =
+        scores_workspace((size_t)num_seqs, (size_t)num_heads, (size_t)head_dim, (size_t)np, (size_t)max_context_len);
+    const DecodeWorkspace& wl = sl.d;
+    const size_t need = with_scores ? sl.total : wl.total;
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 16)) {
+        set_error(": workspace missing, too small (need " + std::to_string(need) +
                   " bytes) or not 16-byte aligned");
         return PA_ERR_INVALID;
     }
@@ -209,6 +218,12 @@ pa_status decode_call(const char* fn, int phases, void* out, const void* q, cons
     if (np > 1) {
         a.ws_acc = reinterpret_cast<float*>(ws + wl.acc);
         a.ws_ml = reinterpret_cast<float*>(ws + wl.ml);
+    }
+    if (with_scores) {
+        a.ws_ml = reinterpret_cast<float*>(ws + sl.ml);
+        a.logits = reinterpret_cast<float*>(ws + sl.logits);
+        a.scores = scores;
+        a.score_stride = score_stride;
     }
     unsigned int* status = nullptr;
     st = status_ptr(&status);
@@ -231,9 +246,9 @@ pa_status decode_call(const char* fn, int phases, void* out, const void* q, cons
     a.num_partitions = np;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.phases = phases;
-    const cudaError_t e =
-        launch_decode(a, dtype, head_dim, block_size, group, static_cast<cudaStream_t>(stream));
-    if (e != cudaSuccess) return cuda_fail((name + " launch").c_str(), e);
+    const cudaError_t e = (with_scores ? launch_decode_scores : launch_decode)(a, dtype, head_dim, block_size,
+                                                                               group, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail((std::string(name) + " launch").c_str(), e);
     return PA_OK;
 }
 
@@ -275,6 +290,106 @@ pa_status pa_decode_run(void* out, const void* q, const void* k_cache, const voi
     return decode_call("pa_decode_run", kDecodeRun, out, q, k_cache, v_cache, block_tables, context_lens, num_seqs,
                        num_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks,
                        max_context_len, scale, partition_size, workspace, workspace_bytes, dtype, stream);
+}
+
+size_t pa_decode_scores_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                       int max_context_len, int partition_size)
+{
+    const int p = pa_decode_partition_size(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len,
+                                           partition_size);
+    if (p <= 0 || num_seqs <= 0 || num_heads <= 0 || head_dim <= 0) return 0;
+    const size_t np = max_context_len > 0 ? ((size_t)max_context_len + p - 1) / p : 1;
+    return scores_workspace((size_t)num_seqs, (size_t)num_heads, (size_t)head_dim, np, (size_t)max_context_len).total;
+}
+
+pa_status pa_decode_scores(void* out, float* scores, const void* q, const void* k_cache, const void* v_cache,
+                           const int32_t* block_tables, const int32_t* context_lens, int num_seqs, int num_heads,
+                           int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq, int num_blocks,
+                           int max_context_len, int score_stride, float scale, int partition_size, void* workspace,
+                           size_t workspace_bytes, pa_dtype dtype, void* stream)
+{
+    pa::CallRange range("pa_decode_scores");
+    return decode_call("pa_decode_scores", kDecodePlan | kDecodeRun, out, q, k_cache, v_cache, block_tables,
+                       context_lens, num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq,
+                       num_blocks, max_context_len, scale, partition_size, workspace, workspace_bytes, dtype, stream,
+                       true, scores, score_stride);
+}
+
+static size_t evict_counts_bytes(size_t rows) { return (rows * sizeof(unsigned) + 255) / 256 * 256; }
+
+size_t pa_evict_workspace_size(int num_seqs, int num_kv_heads, int max_context_len)
+{
+    if (num_seqs <= 0 || num_kv_heads <= 0 || max_context_len < 0 || max_context_len > kMaxEvictContext) return 0;
+    const size_t rows = (size_t)num_seqs * num_kv_heads;
+    return evict_counts_bytes(rows) + rows * sizeof(uint2) * (size_t)std::max(1, max_context_len / 2);
+}
+
+pa_status pa_evict(void* k_cache, void* v_cache, float* new_scores, int32_t* new_positions, const float* scores,
+                   const int32_t* positions, const int32_t* block_tables, const int32_t* context_lens,
+                   const int32_t* keep_lens, int num_recent, int num_seqs, int num_kv_heads, int head_dim,
+                   int block_size, int max_blocks_per_seq, int num_blocks, int max_context_len, int score_stride,
+                   void* workspace, size_t workspace_bytes, pa_dtype dtype, void* stream)
+{
+    pa::CallRange range("pa_evict");
+    pa_status st = check_common("pa_evict", num_kv_heads, head_dim, block_size, num_blocks, dtype);
+    if (st != PA_OK) return st;
+    if (num_recent < 0 || num_seqs < 0 || num_seqs > 65535 || max_blocks_per_seq <= 0 || max_context_len < 0 ||
+        score_stride < max_context_len) {
+        set_error("pa_evict: bad size (score_stride must be at least max_context_len)");
+        return PA_ERR_INVALID;
+    }
+    if (max_context_len > kMaxEvictContext || (int64_t)num_seqs * num_kv_heads > (1 << 20)) {
+        set_error("pa_evict: max_context_len at most " + std::to_string(kMaxEvictContext) +
+                  ", num_seqs * num_kv_heads at most 1048576");
+        return PA_ERR_UNSUPPORTED;
+    }
+    if (num_seqs == 0 || max_context_len == 0) return PA_OK;
+    if (!k_cache || !v_cache || !new_scores || !new_positions || !scores || !positions || !block_tables ||
+        !context_lens || !keep_lens) {
+        set_error("pa_evict: null pointer");
+        return PA_ERR_INVALID;
+    }
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(new_scores, 4) || !aligned(new_positions, 4) ||
+        !aligned(scores, 4) || !aligned(positions, 4) || !aligned(block_tables, 4) || !aligned(context_lens, 4) ||
+        !aligned(keep_lens, 4)) {
+        set_error("pa_evict: misaligned pointer (caches need 16 bytes)");
+        return PA_ERR_INVALID;
+    }
+    const size_t need = pa_evict_workspace_size(num_seqs, num_kv_heads, max_context_len);
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 16)) {
+        set_error("pa_evict: workspace missing, too small (need " + std::to_string(need) +
+                  " bytes) or not 16-byte aligned");
+        return PA_ERR_INVALID;
+    }
+    unsigned int* status = nullptr;
+    st = status_ptr(&status);
+    if (st != PA_OK) return st;
+    EvictArgs a{};
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.new_scores = new_scores;
+    a.new_positions = new_positions;
+    a.scores = scores;
+    a.positions = positions;
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.keep_lens = keep_lens;
+    a.counts = static_cast<unsigned*>(workspace);
+    a.moves = reinterpret_cast<uint2*>(static_cast<unsigned char*>(workspace) +
+                                       evict_counts_bytes((size_t)num_seqs * num_kv_heads));
+    a.status = status;
+    a.num_recent = num_recent;
+    a.num_seqs = num_seqs;
+    a.num_kv_heads = num_kv_heads;
+    a.block_size = block_size;
+    a.max_blocks_per_seq = max_blocks_per_seq;
+    a.num_blocks = num_blocks;
+    a.max_context_len = max_context_len;
+    a.score_stride = score_stride;
+    a.move_stride = std::max(1, max_context_len / 2);
+    const cudaError_t e = launch_evict(a, head_dim, elt_bytes(dtype), static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail("pa_evict launch", e);
+    return PA_OK;
 }
 
 pa_status pa_reshape_and_cache(const void* key, const void* value, void* k_cache, void* v_cache,

@@ -8,9 +8,9 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
-#include <utility>
 
 #include "pa_internal.h"
+#include "pa_launch.cuh"
 #include "pa_ptx.cuh"
 
 namespace pa {
@@ -203,7 +203,9 @@ __global__ void __launch_bounds__(1024) decode_plan_kernel(const DecodeArgs a, i
 // CTA ran before.  The states are summed in tile-phase order (j mod NCW), not in
 // warp order, so the result is the same bits whichever CTA ran the unit and after
 // what: the decode is reproducible run to run under the dynamic work counter.
-template <typename T, int D, int G, int NCW>
+//
+// With STATS the (max, sum) pair goes to the workspace for an unsplit sequence too.
+template <typename T, int D, int G, int NCW, bool STATS>
 __device__ __forceinline__ void finish_unit_warp(const DecodeArgs& a, const float* mg_m, const float* mg_l,
                                                  const float* mg_acc, int s, int kvh, int part, bool split, int rot,
                                                  int lane)
@@ -238,6 +240,11 @@ __device__ __forceinline__ void finish_unit_warp(const DecodeArgs& a, const floa
                 }
             }
             const int h = kvh * G + g;
+            if (STATS && !split && d0 == 0) {
+                const size_t row = ((size_t)s * a.num_heads + h) * a.num_partitions + part;
+                a.ws_ml[row * 2] = M;
+                a.ws_ml[row * 2 + 1] = den;
+            }
             if (!split) {
                 T* o = static_cast<T*>(a.out) + ((size_t)s * a.num_heads + h) * D + d0;
                 const bool any = den > 0.f;
@@ -372,26 +379,6 @@ __global__ void __launch_bounds__(128, 8) decode_merge_kernel(const DecodeArgs a
             for (int k = 0; k < EPL; ++k) o[k] = from_f32<T>(num[k] * inv);
         }
     }
-}
-
-// Launches a kernel with programmatic dependent launch: its CTAs may be scheduled
-// while the previous kernel in the stream drains; they wait (griddepcontrol.wait)
-// before touching that kernel's results.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                       Args&&... args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
 template <typename T, int D>

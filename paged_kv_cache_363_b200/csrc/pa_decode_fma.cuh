@@ -122,8 +122,10 @@ struct FmaConsumer {
     }
 
     // One physical block: K tile kt and V tile vt ([B][D] in shared memory); rows
-    // nvalid.. are past the context and contribute nothing.
-    __device__ __forceinline__ void block(const unsigned char* kt_, unsigned char* vt_, int nvalid)
+    // nvalid.. are past the context and contribute nothing.  LOG: the block's base-2 logits
+    // also go to lg[token][G].
+    template <bool LOG>
+    __device__ __forceinline__ void block(const unsigned char* kt_, unsigned char* vt_, int nvalid, float* lg)
     {
         const T* kt = reinterpret_cast<const T*>(kt_);
         const T* vt = reinterpret_cast<const T*>(vt_);
@@ -152,6 +154,9 @@ struct FmaConsumer {
             for (int k = 0; k < NVO; ++k) {
                 const int t = (idx0 + k) % TPC;
                 const int j = (ch * TPC + t) * RPW + r;
+                if constexpr (LOG) {
+                    if (j < nvalid && (DUP == 1 || c % DUP == 0)) lg[j * G + g_own] = v[k];
+                }
                 if (j >= nvalid) v[k] = -INFINITY;
                 cmax_ = fmaxf(cmax_, v[k]);
             }

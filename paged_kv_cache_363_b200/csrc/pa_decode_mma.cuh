@@ -77,7 +77,7 @@ struct MmaConsumer {
     static constexpr int SCRATCH_FLOATS = 0;
 
     static_assert(D % 64 == 0 && B % 16 == 0, "tile shape");
-    static_assert(G >= 1 && G <= 8, "at most 8 heads on the MMA N side");
+    static_assert(G >= 2 && G <= 8 && G % 2 == 0, "an even number of heads, at most 8, on the MMA N side");
     static_assert(HALF_BYTES % 1024 == 0, "swizzle atoms must stay 1024-byte aligned");
 
     uint32_t qb[DK][2];  // q^T as the B operand: k = head_dim, n = head g
@@ -113,7 +113,9 @@ struct MmaConsumer {
         sl = scale_log2;
     }
 
-    __device__ __forceinline__ void block(const unsigned char* kt_, unsigned char* vt_, int nvalid)
+    // LOG: the tile's base-2 logits also go to lg[token][G].
+    template <bool LOG>
+    __device__ __forceinline__ void block(const unsigned char* kt_, unsigned char* vt_, int nvalid, float* lg)
     {
         const uint32_t kt = smem_u32(kt_);
         const uint32_t vt = smem_u32(vt_);
@@ -144,6 +146,12 @@ struct MmaConsumer {
             }
             const int tok0 = sub * 16 + g;
             float s0 = sc[0] * sl, s1 = sc[1] * sl, s2 = sc[2] * sl, s3 = sc[3] * sl;
+            if constexpr (LOG) {
+                if (2 * t < G) {
+                    if (tok0 < nvalid) *reinterpret_cast<float2*>(lg + tok0 * G + 2 * t) = make_float2(s0, s1);
+                    if (tok0 + 8 < nvalid) *reinterpret_cast<float2*>(lg + (tok0 + 8) * G + 2 * t) = make_float2(s2, s3);
+                }
+            }
             if (tok0 >= nvalid) s0 = s1 = -INFINITY;
             if (tok0 + 8 >= nvalid) s2 = s3 = -INFINITY;
             // ---- online softmax over the sub-tile (max across the 16 token rows of each head)

@@ -57,6 +57,10 @@ struct DecodeArgs {
     int num_partitions;        // NP = ceil(max_context_len / smallest partition tokens)
     float scale_log2;          // scale * log2(e): logits are kept in base-2 units
     int phases;                // host side: kDecodePlan and/or kDecodeRun
+    float* logits;             // pa_decode_scores: [S][Hkv][max_context_len][G] base-2 logits
+    float* scores;             // pa_decode_scores: [S][Hkv][score_stride]
+    int score_stride;
+    int lead_partitions;       // pa_decode_shared: partial states kept for the shared tokens, before a row's own
 };
 
 constexpr int kDecodePlan = 1;  // the plan kernel: work list into the workspace
@@ -99,6 +103,7 @@ bool decode_uses_tensor_cores(pa_dtype dtype, int head_dim, int group);
 // elements, boxes of 64 columns x `box_rows` rows, 128-byte swizzle.
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 cudaError_t tensor_map(CUtensorMap* out, const void* pool, uint64_t rows, int D, int box_rows);
+cudaError_t encode_pool_map(CUtensorMap* out, const void* pool, uint64_t rows, int D, int box_rows);  // no cache
 
 // Process-unique id of the CUDA context current on this thread (cuCtxGetId), or 0
 // when none is current or the driver lacks the call.  Device addresses of the
@@ -106,6 +111,57 @@ cudaError_t tensor_map(CUtensorMap* out, const void* pool, uint64_t rows, int D,
 // reset re-creates the context (and may reload the module elsewhere), which changes
 // the id, so the address is looked up again.
 unsigned long long current_context_id();
+
+// pa_decode_scores: pa_decode's layout (partition statistics always present) and the logits.
+struct ScoresWorkspace {
+    DecodeWorkspace d;
+    size_t ml;         // 8 * S * Hq * NP bytes
+    size_t logits;     // 4 * S * Hq * max_context_len bytes
+    size_t total;
+};
+
+inline ScoresWorkspace scores_workspace(size_t S, size_t Hq, size_t D, size_t NP, size_t max_context)
+{
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    ScoresWorkspace w{};
+    w.d = decode_workspace(S, Hq, D, NP);
+    w.ml = NP > 1 ? w.d.ml : w.d.total;
+    w.logits = up(w.ml + 8 * S * Hq * NP);
+    w.total = up(w.logits + 4 * S * Hq * max_context);
+    return w;
+}
+
+cudaError_t launch_decode_scores(const DecodeArgs& a, pa_dtype dtype, int head_dim, int block_size, int group,
+                                 cudaStream_t stream);
+
+// Eviction (pa_evict.cu).
+constexpr int kMaxEvictContext = 262144;  // two bit masks of the context fit in shared memory
+
+struct EvictArgs {
+    void* k_cache;
+    void* v_cache;
+    float* new_scores;
+    int32_t* new_positions;
+    const float* scores;
+    const int32_t* positions;
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    const int32_t* keep_lens;
+    unsigned* counts;          // [S * Hkv] moves of each (sequence, kv head)
+    uint2* moves;              // [S * Hkv][move_stride] (destination slot, source slot)
+    unsigned int* status;
+    int num_recent;
+    int num_seqs;
+    int num_kv_heads;
+    int block_size;
+    int max_blocks_per_seq;
+    int num_blocks;
+    int max_context_len;
+    int score_stride;
+    int move_stride;           // half of the longest context: a move has a slot on either side of n
+};
+
+cudaError_t launch_evict(const EvictArgs& a, int head_dim, int elt_bytes, cudaStream_t stream);
 
 struct ReshapeArgs {
     const void* key;

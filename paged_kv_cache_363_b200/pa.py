@@ -40,6 +40,10 @@ SIGNATURES = [
     ("pa_decode_plan", _int, [_vp, _vp] + [_int] * 9 + [_vp, _sz, _int, _vp]),
     ("pa_decode_run", _int, [_vp, _vp, _vp, _vp, _vp, _vp] + [_int] * 8 + [_f32, _int, _vp, _sz, _int, _vp]),
     ("pa_decode_static_workspace", _int, [_vp, _vp, _vp, _vp, _vp, _vp] + [_int] * 8 + [_f32, _int, _int, _vp]),
+    ("pa_decode_scores_workspace_size", _sz, [_int] * 7),
+    ("pa_decode_scores", _int, [_vp] * 7 + [_int] * 9 + [_f32, _int, _vp, _sz, _int, _vp]),
+    ("pa_evict_workspace_size", _sz, [_int] * 3),
+    ("pa_evict", _int, [_vp] * 9 + [_int] * 9 + [_vp, _sz, _int, _vp]),
     ("pa_reshape_and_cache", _int, [_vp, _vp, _vp, _vp, _vp] + [_int] * 6 + [_vp]),
     ("pa_prefill", _int, [_vp] * 7 + [_int] * 9 + [_f32, _int, _vp]),
     ("pa_prefill_workspace_size", _sz, []),
@@ -58,6 +62,8 @@ SIGNATURES = [
     ("pa_alloc_append_slot", _int, [_vp, _i64, ctypes.POINTER(_i64), ctypes.POINTER(_i32), ctypes.POINTER(_i32)]),
     ("pa_alloc_append_slots", _int, [_vp, _vp, _int, _vp, _vp, ctypes.POINTER(_int)]),
     ("pa_alloc_beam_step", _int, [_vp, _vp, _int, _vp, _vp, _int, _vp, _vp, ctypes.POINTER(_int)]),
+    ("pa_alloc_make_private", _int, [_vp, _i64, _int, _vp, ctypes.POINTER(_int)]),
+    ("pa_alloc_truncate", _int, [_vp, _i64, _int]),
     ("pa_alloc_free_seq", _int, [_vp, _i64]),
     ("pa_alloc_add_host_pool", _int, [_vp, _int]),
     ("pa_alloc_swap_out", _int, [_vp, _i64, _vp, ctypes.POINTER(_int)]),
@@ -229,6 +235,80 @@ def pa_decode_static_workspace(out, q, k_cache, v_cache, block_tables, context_l
                                         int(partition_size), dt, _stream(stream))
     _check(st, "pa_decode_static_workspace")
     return out
+
+
+def pa_decode_scores_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len,
+                                    partition_size=0):
+    return int(lib.pa_decode_scores_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, block_size,
+                                                   max_context_len, partition_size))
+
+
+def pa_decode_scores(out, scores, q, k_cache, v_cache, block_tables, context_lens, max_context_len, scale,
+                     partition_size=0, workspace=None, stream=None):
+    """pa_decode that also adds every token's attention weight, summed over its kv head's query heads, to
+    scores[S, Hkv, W] (fp32, W >= max_context_len); the last token's entry is set, not added to."""
+    import torch
+    S, Hq, D = q.shape
+    NB, Hkv, B, D2 = k_cache.shape
+    if D2 != D or v_cache.shape != k_cache.shape or out.shape != q.shape:
+        raise ValueError("shape mismatch")
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,):
+        raise ValueError("block_tables must be [S, max_blocks] and context_lens [S]")
+    if scores.dim() != 3 or scores.shape[0] != S or scores.shape[1] != Hkv:
+        raise ValueError("scores must be [S, Hkv, W]")
+    if not (out.dtype == q.dtype == k_cache.dtype == v_cache.dtype):
+        raise TypeError("q, out and the caches must share a dtype")
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise TypeError("block_tables and context_lens must be int32")
+    if scores.dtype != torch.float32:
+        raise TypeError("scores must be float32")
+    if workspace is None:
+        need = pa_decode_scores_workspace_size(S, Hq, Hkv, D, B, int(max_context_len), int(partition_size))
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    st = lib.pa_decode_scores(_dev_ptr(out, "out"), _dev_ptr(scores, "scores"), _dev_ptr(q, "q"),
+                              _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"),
+                              _dev_ptr(block_tables, "block_tables"), _dev_ptr(context_lens, "context_lens"), S, Hq,
+                              Hkv, D, B, block_tables.shape[1], NB, int(max_context_len), scores.shape[2],
+                              float(scale), int(partition_size), _dev_ptr(workspace, "workspace"),
+                              workspace.numel() * workspace.element_size(), _dtype_code(q), _stream(stream))
+    _check(st, "pa_decode_scores")
+    return out
+
+
+def pa_evict_workspace_size(num_seqs, num_kv_heads, max_context_len):
+    return int(lib.pa_evict_workspace_size(num_seqs, num_kv_heads, max_context_len))
+
+
+def pa_evict(k_cache, v_cache, new_scores, new_positions, scores, positions, block_tables, context_lens, keep_lens,
+             num_recent, max_context_len, workspace=None, stream=None):
+    """Keeps, per sequence and kv head, the keep_lens[s] best cached tokens (the num_recent latest positions,
+    then the largest scores) in the first slots; scores/positions[S, Hkv, W] go to new_scores/new_positions,
+    which may be the same tensors.  The caller then shortens the sequences (Allocator.truncate)."""
+    import torch
+    NB, Hkv, B, D = k_cache.shape
+    S = context_lens.shape[0]
+    shape = (S, Hkv, scores.shape[-1])
+    if v_cache.shape != k_cache.shape or any(t.shape != shape for t in (scores, positions, new_scores, new_positions)):
+        raise ValueError("shape mismatch: scores and positions are [S, Hkv, W]")
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or keep_lens.shape != (S,):
+        raise ValueError("block_tables must be [S, max_blocks] and keep_lens [S]")
+    if scores.dtype != torch.float32 or new_scores.dtype != torch.float32:
+        raise TypeError("scores must be float32")
+    if any(t.dtype != torch.int32 for t in (positions, new_positions, block_tables, context_lens, keep_lens)):
+        raise TypeError("positions, block_tables, context_lens and keep_lens must be int32")
+    if k_cache.dtype != v_cache.dtype:
+        raise TypeError("the caches must share a dtype")
+    if workspace is None:
+        need = pa_evict_workspace_size(S, Hkv, int(max_context_len))
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=k_cache.device)
+    st = lib.pa_evict(_dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"), _dev_ptr(new_scores, "new_scores"),
+                      _dev_ptr(new_positions, "new_positions"), _dev_ptr(scores, "scores"),
+                      _dev_ptr(positions, "positions"), _dev_ptr(block_tables, "block_tables"),
+                      _dev_ptr(context_lens, "context_lens"), _dev_ptr(keep_lens, "keep_lens"), int(num_recent), S,
+                      Hkv, D, B, block_tables.shape[1], NB, int(max_context_len), scores.shape[2],
+                      _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+                      _dtype_code(k_cache), _stream(stream))
+    _check(st, "pa_evict")
 
 
 def _host_int64(a):
@@ -442,6 +522,20 @@ class Allocator:
         _check(lib.pa_alloc_beam_step(self._h, _np_ptr(old), old.shape[0], _np_ptr(par), _np_ptr(new), n,
                                       _np_ptr(slots), _np_ptr(pairs), ctypes.byref(ncow)), "pa_alloc_beam_step")
         return slots[:n], pairs[:ncow.value]
+
+    def make_private(self, seq_id, num_tokens):
+        """Replaces the shared or cached blocks of the first num_tokens tokens by fresh ones; returns the
+        (src, dst) pairs to copy before those tokens are changed."""
+        cap = max(1, -(-int(num_tokens) // self.block_size))
+        pairs = np.empty((cap, 2), np.int64)
+        n = _int(0)
+        _check(lib.pa_alloc_make_private(self._h, int(seq_id), int(num_tokens), _np_ptr(pairs), ctypes.byref(n)),
+               "pa_alloc_make_private")
+        return pairs[:n.value]
+
+    def truncate(self, seq_id, num_tokens):
+        """Shortens the sequence to its first num_tokens tokens; the blocks behind them are released."""
+        _check(lib.pa_alloc_truncate(self._h, int(seq_id), int(num_tokens)), "pa_alloc_truncate")
 
     def free_seq(self, seq_id):
         _check(lib.pa_alloc_free_seq(self._h, int(seq_id)), "pa_alloc_free_seq")
