@@ -364,6 +364,42 @@ PA_API pa_status pa_prefill_ws(void* out, const void* q, const void* k_cache, co
                                float scale, void* workspace, size_t workspace_bytes, pa_dtype dtype, void* stream);
 
 /*
+ * Bytes of device workspace pa_cross_attention needs (work entries and, when tokens are
+ * split into chunks, their partial states).  0 on invalid arguments.
+ */
+PA_API size_t pa_cross_attention_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                                int block_size, int num_query_tokens, int max_query_len,
+                                                int max_context_len);
+
+/*
+ * Attention of packed query rows to all cached tokens of their sequence: cross attention to
+ * an encoder's states (or any other tokens that every query may see).  Sequence s holds
+ * context_lens[s] tokens in the pools, whatever its number of query rows, which are rows
+ * q_start[s] .. q_start[s+1]-1 of q [num_query_tokens][num_heads][head_dim]:
+ *   out[row][h] = sum_t softmax_t(scale * q[row][h] . K_t) V_t   over t < context_lens[s],
+ * query head h reading kv head h / (num_heads / num_kv_heads).  A sequence may have no rows
+ * (nothing is written) or no tokens (its rows become zero).  Sums and softmax are fp32; a
+ * weight is rounded to bf16 for its product with V.
+ *   lse        [num_query_tokens][num_heads] fp32 (device, nullable): the natural logarithm
+ *              of the sum of exp(scale * q . K_t), -inf without tokens
+ *   q_start, context_lens  int32 (device), as for pa_prefill; a sequence whose rows leave
+ *              [0, num_query_tokens), run backwards or exceed max_query_len, or whose context
+ *              is negative or past max_context_len or its table row, raises
+ *              PA_DEV_BAD_CONTEXT and is skipped whole
+ *   max_query_len, max_context_len  host-side upper bounds
+ *   workspace  device scratch of pa_cross_attention_workspace_size() bytes, 16-byte aligned;
+ *              no initial contents.  Calls that share it must be ordered on one stream
+ * bf16, head_dim 64 or 128, groups of 1, 2, 4 or 8 (else PA_ERR_UNSUPPORTED).
+ * Asynchronous on stream.
+ */
+PA_API pa_status pa_cross_attention(void* out, float* lse, const void* q, const void* k_cache, const void* v_cache,
+                                    const int32_t* block_tables, const int32_t* context_lens, const int32_t* q_start,
+                                    int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                    int max_blocks_per_seq, int num_blocks, int num_query_tokens, int max_query_len,
+                                    int max_context_len, float scale, void* workspace, size_t workspace_bytes,
+                                    pa_dtype dtype, void* stream);
+
+/*
  * Whole-block copies from one pool to another ([FSAH] "Engineering Limitations":
  * CPU-GPU block swapping under memory pressure): for each (src, dst) pair in
  * block_mapping[num_pairs][2] (int64), block src of src_k_cache / src_v_cache

@@ -13,6 +13,7 @@
 #include <vector>
 
 #include "pa.h"
+#include "pa_group.cuh"
 #include "pa_internal.h"
 
 namespace pa {
@@ -598,6 +599,147 @@ static pa_status prefill_impl(const char* name, void* out, const void* q, const 
     const cudaError_t e =
         launch_prefill(a, group, num_query_tokens, max_query_len, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail("pa_prefill launch", e);
+    return PA_OK;
+}
+
+namespace {
+
+// Layout of pa_cross_attention's workspace: entries and merge list, then the partial states.
+struct CrossWorkspace {
+    GroupWorkspace g;
+    size_t entries, merges, acc, ml, total;
+    int chunks;
+};
+
+CrossWorkspace cross_workspace(size_t S, size_t Hq, int Hkv, int D, size_t Nq, int max_query_len, int max_context_len)
+{
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    CrossWorkspace w{};
+    const int G = (int)(Hq / (size_t)Hkv);
+    const size_t T = 128 / (size_t)G;
+    w.chunks = group_max_chunks(max_context_len, (int64_t)Nq, G, Hkv);
+    w.entries = (S + Nq / T) * (size_t)w.chunks;
+    w.merges = w.chunks > 1 ? Nq : 0;
+    w.g = group_workspace(0, w.entries, w.merges);
+    const size_t states = w.chunks > 1 ? Nq * Hq * (size_t)w.chunks : 0;
+    w.acc = w.g.end;
+    w.ml = up(w.acc + states * (size_t)D * 4);
+    w.total = up(w.ml + states * 8);
+    return w;
+}
+
+// The checks that the two tensor-core calls over packed rows share.
+pa_status check_group(const char* fn, int num_heads, int num_kv_heads, int num_blocks, int block_size, pa_dtype dtype)
+{
+    if (dtype != PA_DTYPE_BF16) {
+        set_error(std::string(fn) + ": bf16 only (the tensor-core tile)");
+        return PA_ERR_UNSUPPORTED;
+    }
+    if (num_heads <= 0 || num_heads % num_kv_heads != 0) {
+        set_error(std::string(fn) + ": num_heads must be a multiple of num_kv_heads");
+        return PA_ERR_INVALID;
+    }
+    const int group = num_heads / num_kv_heads;
+    if (group != 1 && group != 2 && group != 4 && group != 8) {
+        set_error(std::string(fn) + ": num_heads / num_kv_heads must be 1, 2, 4 or 8");
+        return PA_ERR_UNSUPPORTED;
+    }
+    if ((int64_t)num_blocks * num_kv_heads * block_size > (int64_t)INT32_MAX) {
+        set_error(std::string(fn) +
+                  ": num_blocks * num_kv_heads * block_size must stay below 2^31 (tensor-copy row index)");
+        return PA_ERR_UNSUPPORTED;
+    }
+    return PA_OK;
+}
+
+}  // namespace
+
+size_t pa_cross_attention_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                         int num_query_tokens, int max_query_len, int max_context_len)
+{
+    if (num_seqs <= 0 || num_query_tokens <= 0 || max_query_len < 0 || max_context_len < 0 ||
+        check_common("pa_cross_attention_workspace_size", num_kv_heads, head_dim, block_size, 1, PA_DTYPE_BF16) != PA_OK ||
+        check_group("pa_cross_attention_workspace_size", num_heads, num_kv_heads, 1, block_size, PA_DTYPE_BF16) != PA_OK)
+        return 0;
+    return cross_workspace((size_t)num_seqs, (size_t)num_heads, num_kv_heads, head_dim, (size_t)num_query_tokens,
+                           max_query_len, max_context_len)
+        .total;
+}
+
+pa_status pa_cross_attention(void* out, float* lse, const void* q, const void* k_cache, const void* v_cache,
+                             const int32_t* block_tables, const int32_t* context_lens, const int32_t* q_start,
+                             int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                             int max_blocks_per_seq, int num_blocks, int num_query_tokens, int max_query_len,
+                             int max_context_len, float scale, void* workspace, size_t workspace_bytes, pa_dtype dtype,
+                             void* stream)
+{
+    pa::CallRange range("pa_cross_attention");
+    pa_status st = check_common("pa_cross_attention", num_kv_heads, head_dim, block_size, num_blocks, dtype);
+    if (st != PA_OK) return st;
+    st = check_group("pa_cross_attention", num_heads, num_kv_heads, num_blocks, block_size, dtype);
+    if (st != PA_OK) return st;
+    if (num_seqs < 0 || num_seqs > 65535 || num_query_tokens < 0 || max_query_len < 0 || max_context_len < 0 ||
+        max_blocks_per_seq < 0 || !std::isfinite(scale)) {
+        set_error("pa_cross_attention: bad size or scale");
+        return PA_ERR_INVALID;
+    }
+    if (num_seqs == 0 || num_query_tokens == 0 || max_query_len == 0) return PA_OK;
+    if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !q_start) {
+        set_error("pa_cross_attention: null pointer");
+        return PA_ERR_INVALID;
+    }
+    if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(lse, 4) ||
+        !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(q_start, 4)) {
+        set_error("pa_cross_attention: misaligned pointer (q, out, caches need 16 bytes)");
+        return PA_ERR_INVALID;
+    }
+    const CrossWorkspace w = cross_workspace((size_t)num_seqs, (size_t)num_heads, num_kv_heads, head_dim,
+                                             (size_t)num_query_tokens, max_query_len, max_context_len);
+    if (w.entries * (size_t)num_kv_heads > (size_t)INT32_MAX) {
+        set_error("pa_cross_attention: too many query tiles");
+        return PA_ERR_UNSUPPORTED;
+    }
+    if (!workspace || workspace_bytes < w.total || !aligned(workspace, 16)) {
+        set_error("pa_cross_attention: workspace missing, too small (need " + std::to_string(w.total) +
+                  " bytes) or not 16-byte aligned");
+        return PA_ERR_INVALID;
+    }
+    unsigned int* status = nullptr;
+    st = status_ptr(&status);
+    if (st != PA_OK) return st;
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    CrossArgs a{};
+    a.g.out = out;
+    a.g.lse = lse;
+    a.g.q = q;
+    a.g.k_cache = k_cache;
+    a.g.v_cache = v_cache;
+    a.g.block_tables = block_tables;
+    a.g.items = reinterpret_cast<const GroupItem*>(ws + w.g.items);
+    a.g.counts = reinterpret_cast<const unsigned*>(ws + w.g.header);
+    a.g.merge_list = reinterpret_cast<const uint2*>(ws + w.g.merges);
+    a.g.ws_acc = reinterpret_cast<float*>(ws + w.acc);
+    a.g.ws_ml = reinterpret_cast<float*>(ws + w.ml);
+    a.g.status = status;
+    a.g.num_heads = num_heads;
+    a.g.num_kv_heads = num_kv_heads;
+    a.g.max_blocks_per_seq = max_blocks_per_seq;
+    a.g.num_blocks = num_blocks;
+    a.g.block_size = block_size;
+    a.g.num_partitions = w.chunks;
+    a.g.lead_partitions = w.chunks;
+    a.g.max_entries = (int)w.entries;
+    a.g.max_merges = (int)w.merges;
+    a.g.scale_log2 = scale * 1.4426950408889634f;
+    a.context_lens = context_lens;
+    a.q_start = q_start;
+    a.num_seqs = num_seqs;
+    a.num_query_tokens = num_query_tokens;
+    a.max_query_len = max_query_len;
+    a.max_context_len = max_context_len;
+    a.max_chunks = w.chunks;
+    const cudaError_t e = launch_cross(a, head_dim, num_heads / num_kv_heads, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail("pa_cross_attention launch", e);
     return PA_OK;
 }
 

@@ -1,0 +1,732 @@
+// Attention of packed query rows to one block table each, without a mask, on the
+// 5th-generation tensor cores (tcgen05, accumulators in tensor memory), for sm_100a.
+//
+// What it computes: an entry's rows are its members (query tokens) x the G query heads of
+// one kv head, at most 128; all of them attend to the same tokens [kv0, kv0 + kvlen) of one
+// block table.  With x = scale * q . K in base-2 units the rows keep a running maximum m, the
+// sum l of 2^(x - m) and the weighted sum of V rows, and end in out = O / l (and
+// lse = ln 2 * (m + log2 l)), or, when a table's tokens are split into chunks, in the state
+// (m, l, O) that the merge kernel below joins.
+//
+// Few rows share a table (a decode step's requests, one or a few target tokens), so the K/V
+// bytes bound it: every K/V byte is loaded once for all rows of the tile.  A 128-row tile is
+// padded by whatever the group lacks, which costs nothing: a 64-token tile of K and V (32 KB
+// at D = 128) takes 0.74 us at a 148th of the measured copy rate, its two products 0.27 us.
+//
+// A CTA runs units (entry, kv head) b, b + grid, ...; two CTAs per SM, each with
+//   - warp 4: K and V by TMA, one 16-row box per (16-token run of a block, 64 columns),
+//     128-byte swizzle, rings of ST stages that run on across units;
+//   - warp 5 (one thread): S = Q K^T (M = 128, N = 64) into one of two tensor-memory buffers
+//     and O += P V (A = P from tensor memory, V MN-major); S of the next tile is issued before
+//     P V of this one, so the tensor core works while the softmax does;
+//   - warps 0-3: the softmax, a thread per row, which also fetch the rows of Q (cp.async,
+//     swizzled by hand: members may be any rows) while the unit before ends.  Warps without a
+//     valid row only keep the barriers going.
+// P goes as bf16 over its S: one rounding of at most 2^-8 of each weight, which the sum l
+// does not see; it averages out over a row's tokens to the size of the output's own rounding.
+// O is rescaled only when the maximum grows by more than 8 (a weight is then at most 2^8).
+// Every wait is bounded; on expiry the CTA raises PA_DEV_WAIT_TIMEOUT, drains its own copies
+// and MMAs, frees its tensor memory and returns.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <cstring>
+
+#include "pa_group.cuh"
+#include "pa_internal.h"
+#include "pa_launch.cuh"
+#include "pa_ptx.cuh"
+#include "pa_tcgen05.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kRows = 128;      // rows of a tile
+constexpr int kTok = 64;        // tokens per K/V tile
+constexpr int kBox = 16;        // rows per TMA box
+constexpr int kNBox = kTok / kBox;
+constexpr int kThreads = 192;   // 4 softmax warps, producer, MMA issuer
+constexpr int kProdWarp = 4, kMmaWarp = 5;
+constexpr uint32_t kTmemCols = 256;  // S 0..63 and 64..127 (P over their first 32), O 128..
+constexpr float kLazy = 8.f;    // base-2 units
+
+template <int D>
+struct Cfg {
+    static constexpr int NH = D / 64;             // 64-column halves
+    static constexpr int QHALF = kRows * 128;     // bytes of a half of Q
+    static constexpr int KVHALF = kTok * 128;     // bytes of a half of a K or V tile
+    static constexpr int TILE = NH * KVHALF;
+    static constexpr int ST = D == 128 ? 2 : 4;   // stages of K and of V: 64 KB together either way
+    static constexpr int OFF_K = NH * QHALF;
+    static constexpr int OFF_V = OFF_K + ST * TILE;
+    static constexpr int OFF_BAR = OFF_V + ST * TILE;
+    static constexpr int NBAR = 4 * ST + 8;       // k_full, k_empty, v_full, v_empty [ST], q_full, s_full[2], p_full[2],
+                                                  // o_done, o_free, drain
+    static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
+};
+static_assert(2 * (Cfg<128>::SMEM + 1024) <= 227 * 1024, "two CTAs per SM");
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint64_t pack2f(float lo, float hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+
+// (x0, x1) = (s0, s1) * b + c, elementwise over the pairs b and c
+__device__ __forceinline__ void ffma2(float& x0, float& x1, uint32_t s0, uint32_t s1, uint64_t b, uint64_t c)
+{
+    asm("{\n\t.reg .b64 ra, rd;\n\tmov.b64 ra, {%2, %3};\n\t"
+        "fma.rn.f32x2 rd, ra, %4, %5;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(x0), "=f"(x1)
+        : "r"(s0), "r"(s1), "l"(b), "l"(c));
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+__device__ __forceinline__ GroupItem load_item(const GroupArgs& a, unsigned unit)
+{
+    const int4* p = reinterpret_cast<const int4*>(a.items + unit / (unsigned)a.num_kv_heads);
+    const int4 x = __ldcg(p), y = __ldcg(p + 1);
+    GroupItem it;
+    it.table_row = x.x;
+    it.row0 = x.y;
+    it.members = x.z;
+    it.chunk = x.w;
+    it.kv0 = y.x;
+    it.kvlen = y.y;
+    return it;
+}
+
+template <int D, int G>
+__global__ void __launch_bounds__(kThreads, 2)
+    group_attention_kernel(const __grid_constant__ GroupArgs a, const __grid_constant__ CUtensorMap tmap_k,
+                           const __grid_constant__ CUtensorMap tmap_v)
+{
+    using C = Cfg<D>;
+    constexpr int ST = C::ST, NH = C::NH;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    uint64_t* k_empty = k_full + ST;
+    uint64_t* v_full = k_empty + ST;
+    uint64_t* v_empty = v_full + ST;
+    uint64_t* q_full = v_empty + ST;   // a unit's Q written (4 warps)
+    uint64_t* s_full = q_full + 1;     // [2] S = Q K^T in tensor memory
+    uint64_t* p_full = s_full + 2;     // [2] P written (4 warps)
+    uint64_t* o_done = p_full + 2;     // P V finished
+    uint64_t* o_free = o_done + 1;     // a unit's O read out (4 warps)
+    uint64_t* drain = o_free + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(drain + 1) + 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(&k_full[i], 1);
+            mbar_init(&k_empty[i], 1);
+            mbar_init(&v_full[i], 1);
+            mbar_init(&v_empty[i], 1);
+        }
+        mbar_init(q_full, 4);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);
+        }
+        mbar_init(o_done, 1);
+        mbar_init(o_free, 4);
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) tmem_alloc(tmem_slot, kTmemCols);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait_primary();       // the plan's entries are visible from here on
+    pdl_launch_dependents();  // after it: a kernel that only needs the plan may start now
+    const unsigned nunits = __ldcg(a.counts) * (unsigned)a.num_kv_heads;
+
+    if (warp == kProdWarp) {
+        const uint64_t pol = policy_evict_normal();
+        bool ok = true;
+        int t = 0, nk = 0, nv = 0;  // tiles of finished units; K and V tiles issued
+        const int box = lane % kNBox, half = lane / kNBox;
+        for (unsigned u = blockIdx.x; u < nunits && ok; u += gridDim.x) {
+            const GroupItem it = load_item(a, u);
+            const int kvh = (int)(u % (unsigned)a.num_kv_heads);
+            const int32_t* table = a.block_tables + (size_t)it.table_row * a.max_blocks_per_seq;
+            const int n = (it.kvlen + kTok - 1) / kTok;
+            auto lookup = [&](int j) -> int {
+                const int tok = j * kTok + box * kBox;
+                return j < n && half < NH && tok < it.kvlen ? __ldg(table + (it.kv0 + tok) / a.block_size) : 0;
+            };
+            int next = lookup(0);
+            for (int j = 0; j < n; ++j, ++t) {
+                int phys = next;
+                next = lookup(j + 1);
+                const int nbox = min(kNBox, (it.kvlen - j * kTok + kBox - 1) / kBox);
+                const bool mine = half < NH && box < nbox;
+                if (mine && (unsigned)phys >= (unsigned)a.num_blocks) {
+                    atomicOr(a.status, PA_DEV_BAD_BLOCK);
+                    phys = 0;
+                }
+                const int row = (phys * a.num_kv_heads + kvh) * a.block_size +
+                                (it.kv0 + j * kTok + box * kBox) % a.block_size;
+                const uint32_t tx = (uint32_t)(nbox * kBox * 128 * NH);
+                const int st = t % ST;
+                const uint32_t off = st * C::TILE + half * C::KVHALF + box * kBox * 128;
+                if (lane == 0) {
+                    if (t >= ST && !mbar_wait_bounded(&k_empty[st], ((t / ST) & 1) ^ 1, abort_flag)) ok = false;
+                    if (ok) mbar_arrive_expect_tx(&k_full[st], tx);
+                }
+                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                if (!ok) break;
+                if (mine) tma_load_2d(smem_u32(smem + C::OFF_K + off), &tmap_k, half * 64, row, &k_full[st], pol);
+                ++nk;
+                if (lane == 0) {
+                    if (t >= ST && !mbar_wait_bounded(&v_empty[st], ((t / ST) & 1) ^ 1, abort_flag)) ok = false;
+                    if (ok) mbar_arrive_expect_tx(&v_full[st], tx);
+                }
+                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                if (!ok) break;
+                if (mine) tma_load_2d(smem_u32(smem + C::OFF_V + off), &tmap_v, half * 64, row, &v_full[st], pol);
+                ++nv;
+            }
+        }
+        if (lane == 0) {
+            if (!ok) {
+                atomicOr(a.status, PA_DEV_WAIT_TIMEOUT);
+                *abort_flag = 1;
+            }
+            // nothing may still be landing in shared memory when the CTA exits
+            volatile int never = 0;
+            for (int i = max(0, nk - ST); i < nk; ++i)
+                if (!mbar_wait_bounded(&k_full[i % ST], (i / ST) & 1, &never)) atomicOr(a.status, PA_DEV_WAIT_TIMEOUT);
+            for (int i = max(0, nv - ST); i < nv; ++i)
+                if (!mbar_wait_bounded(&v_full[i % ST], (i / ST) & 1, &never)) atomicOr(a.status, PA_DEV_WAIT_TIMEOUT);
+        }
+    } else if (warp == kMmaWarp) {
+        if (lane == 0) {
+            constexpr uint32_t idesc_qk = umma_idesc_bf16(kRows, kTok, false);
+            constexpr uint32_t idesc_pv = umma_idesc_bf16(kRows, D, true);
+            const uint32_t sq = smem_u32(smem), sk = smem_u32(smem + C::OFF_K), sv = smem_u32(smem + C::OFF_V);
+            // S of tile t (the K stages' position), `first`: its unit's Q has to be waited for
+            int units = 0;  // units whose first S was issued
+            auto issue_qk = [&](int t, bool first) -> bool {
+                // The buffer held P of tile t - 2: after its P V has finished.  Inside a unit that is
+                // the last one issued; at a unit's start P V of tile t - 1 is issued too, and a one-bit
+                // parity is only good for the last one, so that one is waited for.
+                const int last = first ? t - 1 : t - 2;
+                if (last >= 0 && !mbar_wait_bounded(o_done, last & 1, abort_flag)) return false;
+                if (first && !mbar_wait_bounded(q_full, units++ & 1, abort_flag)) return false;
+                if (!mbar_wait_bounded(&k_full[t % ST], (t / ST) & 1, abort_flag)) return false;
+                tc_fence_after_sync();
+                const uint32_t kb = sk + (t % ST) * C::TILE;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t kk = (k & 3) * 32;
+                    umma_bf16_ss(tmem + (t & 1) * kTok, umma_desc_sw128(sq + (k >> 2) * C::QHALF + kk, 16, 1024),
+                                 umma_desc_sw128(kb + (k >> 2) * C::KVHALF + kk, 16, 1024), idesc_qk, k > 0 ? 1u : 0u);
+                }
+                umma_commit(&s_full[t & 1]);
+                umma_commit(&k_empty[t % ST]);
+                return true;
+            };
+            bool ok = true;
+            int t = 0;       // tiles whose P V was issued
+            int done = 0;    // units finished
+            unsigned u = blockIdx.x;
+            auto tiles_of = [&](unsigned unit) { return (load_item(a, unit).kvlen + kTok - 1) / kTok; };
+            int n = 0;
+            for (; u < nunits; u += gridDim.x)
+                if ((n = tiles_of(u)) > 0) break;
+            if (u < nunits) ok = issue_qk(0, true);
+            while (ok && u < nunits) {
+                // the next unit with tokens
+                unsigned un = u + gridDim.x;
+                int nn = 0;
+                for (; un < nunits; un += gridDim.x)
+                    if ((nn = tiles_of(un)) > 0) break;
+                for (int j = 0; j < n && ok; ++j, ++t) {
+                    if (j + 1 < n && !(ok = issue_qk(t + 1, false))) break;
+                    if (!mbar_wait_bounded(&p_full[t & 1], (t >> 1) & 1, abort_flag) ||
+                        (j == 0 && done > 0 && !mbar_wait_bounded(o_free, (done - 1) & 1, abort_flag)) ||
+                        !mbar_wait_bounded(&v_full[t % ST], (t / ST) & 1, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    const uint32_t vb = sv + (t % ST) * C::TILE, p = tmem + (t & 1) * kTok;
+#pragma unroll
+                    for (int k = 0; k < kTok / 16; ++k)
+                        umma_bf16_ts(tmem + 128, p + k * 8, umma_desc_sw128(vb + k * 16 * 128, C::KVHALF, 1024), idesc_pv,
+                                     (j > 0 || k > 0) ? 1u : 0u);
+                    umma_commit(o_done);
+                    umma_commit(&v_empty[t % ST]);
+                }
+                ++done;
+                u = un;
+                n = nn;
+                if (ok && u < nunits) ok = issue_qk(t, true);
+            }
+            if (!ok) {
+                atomicOr(a.status, PA_DEV_WAIT_TIMEOUT);
+                *abort_flag = 1;
+            }
+            umma_commit(drain);
+            volatile int never = 0;
+            if (!mbar_wait_bounded(drain, 0, &never)) atomicOr(a.status, PA_DEV_WAIT_TIMEOUT);
+        }
+    } else {
+        const int r = threadIdx.x;  // row of the tile
+        const int member = r / G, head = r % G;
+        const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+        const bool neg = a.scale_log2 < 0.f;
+        const float sl = neg ? -a.scale_log2 : a.scale_log2;
+        const uint64_t slp = pack2f(sl, sl);
+        bool ok = true;
+        int t = 0, done = 0;
+        auto query_row = [&](const GroupItem& it) {
+            const int i = it.row0 + min(member, it.members - 1);
+            return a.rows ? __ldg(a.rows + i) : i;
+        };
+        // this row of the unit's Q into shared memory, 16 bytes at a time
+        auto fetch_q = [&](int row, int kvh) {
+            const char* src = static_cast<const char*>(a.q) +
+                              (((size_t)row * a.num_heads) + (size_t)kvh * G + head) * (D * 2);
+            const uint32_t dst = smem_u32(smem) + r * 128;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c)
+                cp_async16(dst + (c >> 3) * C::QHALF + (((c & 7) ^ (r & 7)) << 4), src + c * 16);
+        };
+        auto q_ready = [&]() {
+            cp_async_wait_all();
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
+        };
+        // the first unit from u on that has tokens; rows of the others get zeros
+        auto settle = [&](unsigned u, GroupItem& it) -> unsigned {
+            for (; u < nunits; u += gridDim.x) {
+                it = load_item(a, u);
+                if (it.kvlen > 0) break;
+                if (member < it.members) {
+                    const size_t o = (size_t)query_row(it) * a.num_heads + (u % (unsigned)a.num_kv_heads) * G + head;
+                    uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + o * D);
+                    for (int c = 0; c < D / 8; ++c) out[c] = make_uint4(0, 0, 0, 0);
+                    if (a.lse) a.lse[o] = -INFINITY;
+                }
+            }
+            return u;
+        };
+        GroupItem it;
+        unsigned u = settle(blockIdx.x, it);
+        int row = 0;
+        if (u < nunits) {
+            row = query_row(it);
+            fetch_q(row, (int)(u % (unsigned)a.num_kv_heads));
+            q_ready();
+        }
+        while (u < nunits) {
+            const int kvh = (int)(u % (unsigned)a.num_kv_heads);
+            const int n = (it.kvlen + kTok - 1) / kTok;
+            const bool valid = member < it.members;
+            const bool active = (warp * 32) / G < it.members;  // the warp has a valid row
+            GroupItem nit;
+            const unsigned un = settle(u + gridDim.x, nit);
+            const int nrow = un < nunits ? query_row(nit) : 0;
+            float m_used = -INFINITY, l = 0.f;
+            for (int j = 0; j < n; ++j, ++t) {
+                if (!mbar_wait_warp(&s_full[t & 1], (t >> 1) & 1, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after_sync();
+                // every Q K^T of the unit has finished: the next unit's Q may take its place
+                if (j == n - 1 && un < nunits) fetch_q(nrow, (int)(un % (unsigned)a.num_kv_heads));
+                const int left = it.kvlen - j * kTok;  // tokens from this tile on
+                if (active) {
+                    uint32_t sr[2][32];
+                    tmem_ld32(tmem + (t & 1) * kTok + lane_base, sr[0]);
+                    tmem_ld32(tmem + (t & 1) * kTok + 32 + lane_base, sr[1]);
+                    tmem_wait_ld();
+                    if (neg) {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) sr[c][e] ^= 0x80000000u;
+                    }
+                    if (left < kTok) {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (c * 32 + e >= left) sr[c][e] = __float_as_uint(-INFINITY);
+                    }
+                    float mx[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) mx[i] = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) mx[e & 7] = fmaxf(mx[e & 7], __uint_as_float(sr[c][e]));
+                    const float mraw = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                             fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+                    const float m_new = fmaxf(m_used, mraw == -INFINITY ? -INFINITY : mraw * sl);
+                    const bool rescale = m_used != -INFINITY && m_new > m_used + kLazy;
+                    const float alpha = rescale ? ex2(m_used - m_new) : 1.f;
+                    if (rescale || m_used == -INFINITY) m_used = m_new;
+                    const float mref = m_used == -INFINITY ? 0.f : m_used;
+                    const uint64_t mrp = pack2f(-mref, -mref);
+                    float rs[4] = {0.f, 0.f, 0.f, 0.f};
+                    uint32_t p[32];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            float x0, x1;
+                            ffma2(x0, x1, sr[c][2 * e], sr[c][2 * e + 1], slp, mrp);
+                            float p0 = ex2(x0), p1 = ex2(x1);
+                            if (left < kTok) {  // (-inf * 0 is no -inf: a scale of zero)
+                                p0 = c * 32 + 2 * e < left ? p0 : 0.f;
+                                p1 = c * 32 + 2 * e + 1 < left ? p1 : 0.f;
+                            }
+                            rs[(e & 1) * 2] += p0;
+                            rs[(e & 1) * 2 + 1] += p1;
+                            p[c * 16 + e] = pack_bf16(p0, p1);
+                        }
+                    tmem_st32(tmem + (t & 1) * kTok + lane_base, p);
+                    l = l * alpha + ((rs[0] + rs[1]) + (rs[2] + rs[3]));
+                    if (__any_sync(0xffffffffu, rescale)) {
+                        // O may be changed once the last P V has finished
+                        if (!mbar_wait_warp(o_done, (t - 1) & 1, abort_flag)) ok = false;
+                        tc_fence_after_sync();
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t o[32];
+                            tmem_ld32(tmem + 128 + lane_base + c * 32, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            tmem_st32(tmem + 128 + lane_base + c * 32, o);
+                        }
+                    }
+                    tmem_wait_st();
+                }
+                if (!ok) break;
+                if (left < kTok) {
+                    // rows past the tokens: their weight is 0, and 0 must not meet a NaN left in the pool
+                    if (!mbar_wait_warp(&v_full[t % ST], (t / ST) & 1, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    for (int i = r; i < (kTok - left) * NH * 8; i += 128) {
+                        const int vr = left + i / (NH * 8), h = (i >> 3) % NH;
+                        *reinterpret_cast<uint4*>(smem + C::OFF_V + (t % ST) * C::TILE + h * C::KVHALF + vr * 128 +
+                                                  (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_async_smem();
+                }
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[t & 1]);
+            }
+            if (!ok) break;
+            if (un < nunits) q_ready();
+            if (!mbar_wait_warp(o_done, (t - 1) & 1, abort_flag)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after_sync();
+            if (active) {
+                const size_t o_row = (size_t)row * a.num_heads + (size_t)kvh * G + head;
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32(tmem + 128 + lane_base + c * 32, o);
+                    tmem_wait_ld();
+                    if (valid && it.chunk < 0) {
+                        uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + o_row * D + c * 32);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint4 pk;
+                            pk.x = pack_bf16(__uint_as_float(o[e * 8 + 0]) * inv, __uint_as_float(o[e * 8 + 1]) * inv);
+                            pk.y = pack_bf16(__uint_as_float(o[e * 8 + 2]) * inv, __uint_as_float(o[e * 8 + 3]) * inv);
+                            pk.z = pack_bf16(__uint_as_float(o[e * 8 + 4]) * inv, __uint_as_float(o[e * 8 + 5]) * inv);
+                            pk.w = pack_bf16(__uint_as_float(o[e * 8 + 6]) * inv, __uint_as_float(o[e * 8 + 7]) * inv);
+                            out[e] = pk;
+                        }
+                    } else if (valid) {
+                        uint4* acc = reinterpret_cast<uint4*>(
+                            a.ws_acc + (o_row * a.num_partitions + it.chunk) * D + c * 32);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) acc[e] = make_uint4(o[e * 4], o[e * 4 + 1], o[e * 4 + 2], o[e * 4 + 3]);
+                    }
+                }
+                if (valid) {
+                    if (it.chunk >= 0) {
+                        *reinterpret_cast<float2*>(a.ws_ml + (o_row * a.num_partitions + it.chunk) * 2) =
+                            make_float2(m_used, l);
+                    } else if (a.lse) {
+                        a.lse[o_row] = (m_used + log2f(l)) * 0.6931471805599453f;
+                    }
+                }
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(o_free);
+            ++done;
+            u = un;
+            it = nit;
+            row = nrow;
+        }
+        if (!ok) {
+            cp_async_wait_all();
+            if (lane == 0) atomicOr(a.status, PA_DEV_WAIT_TIMEOUT);
+            *abort_flag = 1;
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+// Joins the partial states of the listed rows, a warp per (row, query head): M = max m_p,
+// out = sum 2^(m_p - M) acc_p / sum 2^(m_p - M) l_p, in list order of the states.  Eight
+// states are in flight at a time; a lane owns D / 32 columns.
+template <int D>
+__global__ void __launch_bounds__(128) group_merge_kernel(const GroupArgs a)
+{
+    constexpr int EPL = D / 32, CH = 8;
+    pdl_wait_primary();
+    const int lane = threadIdx.x & 31;
+    const unsigned total = __ldcg(a.counts + 1) * (unsigned)a.num_heads;
+    for (unsigned w = blockIdx.x * 4 + (threadIdx.x >> 5); w < total; w += gridDim.x * 4) {
+        const uint2 e = __ldcg(a.merge_list + w / (unsigned)a.num_heads);
+        const int h = (int)(w % (unsigned)a.num_heads);
+        const int nl = (int)(e.y & 0xffffu), np = nl + (int)(e.y >> 16);
+        const size_t row = (size_t)e.x * a.num_heads + h;
+        const float2* ml = reinterpret_cast<const float2*>(a.ws_ml) + row * a.num_partitions;
+        const float* acc = a.ws_acc + row * a.num_partitions * D + lane * EPL;
+        auto slot = [&](int p) { return p < nl ? p : a.lead_partitions + p - nl; };
+        float M = -INFINITY;
+        for (int p = lane; p < np; p += 32) M = fmaxf(M, __ldcg(ml + slot(p)).x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        float num[EPL], den = 0.f;
+#pragma unroll
+        for (int k = 0; k < EPL; ++k) num[k] = 0.f;
+        for (int c = 0; c < np; c += CH) {
+            float x[CH][EPL];
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                const float* src = acc + (size_t)slot(min(c + i, np - 1)) * D;
+                if constexpr (EPL == 4) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+                    x[i][0] = v.x; x[i][1] = v.y; x[i][2] = v.z; x[i][3] = v.w;
+                } else {
+                    const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+                    x[i][0] = v.x; x[i][1] = v.y;
+                }
+            }
+            float wt = 0.f;  // lane i < 8: the weight of state c + i
+            if (lane < CH && c + lane < np) {
+                const float2 v = __ldcg(ml + slot(c + lane));
+                wt = v.x == -INFINITY ? 0.f : exp2f(v.x - M);
+                den = fmaf(wt, v.y, den);
+            }
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                const float wi = __shfl_sync(0xffffffffu, wt, i);
+                if (wi != 0.f) {  // (a state without tokens has no values)
+#pragma unroll
+                    for (int k = 0; k < EPL; ++k) num[k] = fmaf(wi, x[i][k], num[k]);
+                }
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+        const float inv = den > 0.f ? 1.f / den : 0.f;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + row * D + lane * EPL;
+        if constexpr (EPL == 4) {
+            uint2 pk;
+            pk.x = pack_bf16(num[0] * inv, num[1] * inv);
+            pk.y = pack_bf16(num[2] * inv, num[3] * inv);
+            *reinterpret_cast<uint2*>(out) = pk;
+        } else {
+            *reinterpret_cast<uint32_t*>(out) = pack_bf16(num[0] * inv, num[1] * inv);
+        }
+        if (a.lse && lane == 0) a.lse[row] = den > 0.f ? (M + log2f(den)) * 0.6931471805599453f : -INFINITY;
+    }
+}
+
+// pa_cross_attention's plan: one entry per (sequence, tile of 128 / G query tokens, chunk of
+// its tokens), the tiles of a chunk next to each other (they read the same K/V), and the
+// query rows of sequences with several chunks for the merge.  The chunk length is the work
+// (tokens x tiles x kv heads) over twice the resident CTAs, at least 256 tokens.
+constexpr int kPlanThreads = 1024;
+
+__global__ void __launch_bounds__(kPlanThreads) cross_plan_kernel(const CrossArgs a, int group, int ctas)
+{
+    __shared__ unsigned long long s_work;
+    __shared__ unsigned s_items, s_merges;
+    pdl_launch_dependents();
+    const int T = kRows / group;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cap = min(a.max_context_len, (int)min((long long)a.g.max_blocks_per_seq * a.g.block_size, 0x7fffffffll));
+    if (threadIdx.x == 0) {
+        s_work = 0;
+        s_items = s_merges = 0;
+    }
+    __syncthreads();
+    unsigned long long work = 0;
+    for (int s = threadIdx.x; s < a.num_seqs; s += kPlanThreads) {
+        const int q0 = __ldg(a.q_start + s), q1 = __ldg(a.q_start + s + 1), L = __ldg(a.context_lens + s);
+        if (q0 < 0 || q1 > a.num_query_tokens || q1 < q0 || q1 - q0 > a.max_query_len || L < 0 || L > cap)
+            atomicOr(a.g.status, PA_DEV_BAD_CONTEXT);
+        else
+            work += (unsigned long long)((q1 - q0 + T - 1) / T) * L;
+    }
+    if (work) atomicAdd(&s_work, work);
+    __syncthreads();
+    const unsigned long long share = s_work * a.g.num_kv_heads / (2ull * ctas);
+    const int least = (a.max_context_len + a.max_chunks - 1) / a.max_chunks;
+    const int chunk = (max(max((int)min(share, 1ull << 30), least), 256) + kTok - 1) / kTok * kTok;
+    GroupItem* items = const_cast<GroupItem*>(a.g.items);
+    uint2* merges = const_cast<uint2*>(a.g.merge_list);
+    for (int s = warp; s < a.num_seqs; s += kPlanThreads / 32) {
+        const int q0 = __ldg(a.q_start + s), q1 = __ldg(a.q_start + s + 1), L = __ldg(a.context_lens + s);
+        const int rows = q1 - q0;
+        if (q0 < 0 || q1 > a.num_query_tokens || rows <= 0 || rows > a.max_query_len || L < 0 || L > cap) continue;
+        const int tiles = (rows + T - 1) / T;
+        const int want = max(1, (L + chunk - 1) / chunk);
+        const int per = max(1, ((L + want - 1) / want + kTok - 1) / kTok) * kTok;
+        const int nch = max(1, (L + per - 1) / per);
+        unsigned i0 = 0, m0 = 0;
+        if (lane == 0) {
+            i0 = atomicAdd(&s_items, (unsigned)(tiles * nch));
+            m0 = nch > 1 ? atomicAdd(&s_merges, (unsigned)rows) : 0u;
+        }
+        i0 = __shfl_sync(0xffffffffu, i0, 0);
+        m0 = __shfl_sync(0xffffffffu, m0, 0);
+        // rows listed twice (q_start running backwards elsewhere) can ask for more than there is room for
+        if (i0 + tiles * nch > (unsigned)a.g.max_entries || (nch > 1 && m0 + rows > (unsigned)a.g.max_merges)) {
+            if (lane == 0) atomicOr(a.g.status, PA_DEV_BAD_CONTEXT);
+            for (unsigned i = i0 + lane; i < min(i0 + tiles * nch, (unsigned)a.g.max_entries); i += 32)
+                items[i] = GroupItem{0, 0, 0, 0, 0, 0, {0, 0}};
+            for (unsigned i = m0 + lane; nch > 1 && i < min(m0 + rows, (unsigned)a.g.max_merges); i += 32)
+                merges[i] = make_uint2((unsigned)q0, 0u);
+            continue;
+        }
+        for (int i = lane; i < tiles * nch; i += 32) {
+            const int ch = i / tiles, tile = i % tiles;
+            GroupItem it{};
+            it.table_row = s;
+            it.row0 = q0 + tile * T;
+            it.members = min(T, rows - tile * T);
+            it.chunk = nch > 1 ? ch : -1;
+            it.kv0 = ch * per;
+            it.kvlen = min(per, L - ch * per);
+            items[i0 + i] = it;
+        }
+        if (nch > 1)
+            for (int i = lane; i < rows; i += 32) merges[m0 + i] = make_uint2((unsigned)(q0 + i), (unsigned)nch);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        unsigned* counts = const_cast<unsigned*>(a.g.counts);
+        counts[0] = min(s_items, (unsigned)a.g.max_entries);
+        counts[1] = min(s_merges, (unsigned)a.g.max_merges);
+    }
+}
+
+int sm_count()
+{
+    int dev = 0, sms = 148;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    return sms;
+}
+
+template <int D, int G>
+cudaError_t launch_group_dg(const GroupArgs& a, cudaStream_t stream)
+{
+    using C = Cfg<D>;
+    CUtensorMap tk, tv;
+    const uint64_t rows = (uint64_t)a.num_blocks * a.num_kv_heads * a.block_size;
+    cudaError_t e = encode_pool_map(&tk, a.k_cache, rows, D, kBox);
+    if (e != cudaSuccess) return e;
+    if ((e = encode_pool_map(&tv, a.v_cache, rows, D, kBox)) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(group_attention_kernel<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  C::SMEM)) != cudaSuccess)
+        return e;
+    const int64_t units = (int64_t)a.max_entries * a.num_kv_heads;
+    const unsigned grid = (unsigned)std::min<int64_t>(units, group_resident_ctas(sm_count()));
+    return launch_pdl(group_attention_kernel<D, G>, dim3(grid), dim3(kThreads), (size_t)C::SMEM, stream, a, tk, tv);
+}
+
+template <int D>
+cudaError_t launch_group_d(const GroupArgs& a, int group, cudaStream_t stream)
+{
+    switch (group) {
+        case 1: return launch_group_dg<D, 1>(a, stream);
+        case 2: return launch_group_dg<D, 2>(a, stream);
+        case 4: return launch_group_dg<D, 4>(a, stream);
+        case 8: return launch_group_dg<D, 8>(a, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+int group_resident_ctas(int sms) { return 2 * sms; }
+
+cudaError_t launch_group(const GroupArgs& a, int head_dim, int group, cudaStream_t stream)
+{
+    return head_dim == 64 ? launch_group_d<64>(a, group, stream) : launch_group_d<128>(a, group, stream);
+}
+
+cudaError_t launch_group_merge(const GroupArgs& a, int head_dim, cudaStream_t stream)
+{
+    const int64_t ctas = ((int64_t)a.max_merges * a.num_heads + 3) / 4;
+    const unsigned grid = (unsigned)std::min<int64_t>(ctas, 16LL * sm_count());
+    return head_dim == 64 ? launch_pdl(group_merge_kernel<64>, dim3(grid), dim3(128), 0, stream, a)
+                          : launch_pdl(group_merge_kernel<128>, dim3(grid), dim3(128), 0, stream, a);
+}
+
+cudaError_t launch_cross(const CrossArgs& a, int head_dim, int group, cudaStream_t stream)
+{
+    cross_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, group, group_resident_ctas(sm_count()));
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    if ((e = launch_group(a.g, head_dim, group, stream)) != cudaSuccess) return e;
+    return a.max_chunks > 1 ? launch_group_merge(a.g, head_dim, stream) : cudaSuccess;
+}
+
+}  // namespace pa

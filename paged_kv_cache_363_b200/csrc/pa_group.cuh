@@ -1,0 +1,98 @@
+// Attention of packed query rows to one block table each, without a mask: the tensor-core
+// kernel that pa_cross_attention and the shared tokens of pa_decode_shared run on, its work
+// entries, and the merge of a row's partial states.
+#pragma once
+
+#include <cstdint>
+
+#include "pa_internal.h"
+
+namespace pa {
+
+// One entry: the members (query tokens) that share a 128-row tile, and the tokens they attend to.
+struct GroupItem {
+    int table_row;   // row of block_tables
+    int row0;        // first member: an index into rows[] (or the query row itself when rows is null)
+    int members;     // at most 128 / G
+    int chunk;       // partial state this entry writes, or -1: it writes the output
+    int kv0, kvlen;  // tokens [kv0, kv0 + kvlen); kv0 a multiple of 64
+    int pad[2];
+};
+
+struct GroupArgs {
+    void* out;                    // [rows][num_heads][D] bf16
+    float* lse;                   // [rows][num_heads] or null
+    const void* q;                // [rows][num_heads][D] bf16
+    const void* k_cache;
+    const void* v_cache;
+    const int32_t* block_tables;
+    const int32_t* rows;          // query row of each member, or null
+    const GroupItem* items;
+    const unsigned* counts;       // [0] entries, [1] rows to merge
+    const uint2* merge_list;      // (row, first partial states | own partial states << 16)
+    float* ws_acc;                // [rows][num_heads][num_partitions][D]
+    float* ws_ml;                 // [rows][num_heads][num_partitions][2]
+    unsigned int* status;
+    int num_heads;
+    int num_kv_heads;
+    int max_blocks_per_seq;
+    int num_blocks;
+    int block_size;
+    int num_partitions;           // partial states kept per (row, head)
+    int lead_partitions;          // of them, those of the tokens all members share (the others follow)
+    int max_entries;              // host bounds: entries, and rows to merge
+    int max_merges;
+    float scale_log2;
+};
+
+// Bytes of the entries, the merge list and the header, from a 256-byte aligned base.
+struct GroupWorkspace {
+    size_t header, items, merges, end;
+};
+
+inline GroupWorkspace group_workspace(size_t base, size_t max_entries, size_t max_merges)
+{
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    GroupWorkspace w{};
+    w.header = base;
+    w.items = base + 256;
+    w.merges = up(w.items + max_entries * sizeof(GroupItem));
+    w.end = up(w.merges + max_merges * sizeof(uint2));
+    return w;
+}
+
+// Most chunks a table's tokens are split into: enough that about 1200 units exist (four per
+// resident CTA) whatever the batch, chunks of 256 tokens or more, at most 32.
+inline int group_max_chunks(int64_t max_len, int64_t rows, int group, int num_kv_heads)
+{
+    const int64_t by_len = (max_len + 255) / 256;
+    const int64_t tiles = rows * group / 128 > 1 ? rows * group / 128 : 1;
+    const int64_t want = (1200 + num_kv_heads * tiles - 1) / (num_kv_heads * tiles);
+    int64_t n = by_len < want ? by_len : want;
+    n = n < 1 ? 1 : n;
+    return (int)(n < 32 ? n : 32);
+}
+
+// CTAs of the kernel resident on the device at once.
+int group_resident_ctas(int sms);
+
+// The kernel over the entries a plan kernel (just launched on the stream) wrote; then, when
+// `merge` is set, the merge of the rows it listed.
+cudaError_t launch_group(const GroupArgs& a, int head_dim, int group, cudaStream_t stream);
+cudaError_t launch_group_merge(const GroupArgs& a, int head_dim, cudaStream_t stream);
+
+// pa_cross_attention: plan, kernel, merge.
+struct CrossArgs {
+    GroupArgs g;
+    const int32_t* context_lens;
+    const int32_t* q_start;
+    int num_seqs;
+    int num_query_tokens;
+    int max_query_len;
+    int max_context_len;
+    int max_chunks;
+};
+
+cudaError_t launch_cross(const CrossArgs& a, int head_dim, int group, cudaStream_t stream);
+
+}  // namespace pa

@@ -48,6 +48,8 @@ SIGNATURES = [
     ("pa_prefill", _int, [_vp] * 7 + [_int] * 9 + [_f32, _int, _vp]),
     ("pa_prefill_workspace_size", _sz, []),
     ("pa_prefill_ws", _int, [_vp] * 7 + [_int] * 9 + [_f32, _vp, _sz, _int, _vp]),
+    ("pa_cross_attention_workspace_size", _sz, [_int] * 8),
+    ("pa_cross_attention", _int, [_vp] * 8 + [_int] * 10 + [_f32, _vp, _sz, _int, _vp]),
     ("pa_copy_blocks", _int, [_vp, _vp, _vp] + [_int] * 6 + [_vp]),
     ("pa_check_block_mapping", _int, [_vp, _int, _int]),
     ("pa_check_slot_mapping", _int, [_vp, _int, _int, _int]),
@@ -388,6 +390,45 @@ def pa_prefill(out, q, k_cache, v_cache, block_tables, context_lens, q_start, ma
         nbytes = workspace.numel() * workspace.element_size()
         _check(lib.pa_prefill_ws(*args, _dev_ptr(workspace, "workspace"), nbytes, dt, _stream(stream)),
                "pa_prefill_ws")
+
+
+def pa_cross_attention_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, block_size, num_query_tokens,
+                                      max_query_len, max_context_len):
+    return int(lib.pa_cross_attention_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, block_size,
+                                                     num_query_tokens, max_query_len, max_context_len))
+
+
+def pa_cross_attention(out, q, k_cache, v_cache, block_tables, context_lens, q_start, max_query_len, max_context_len,
+                       scale, lse=None, workspace=None, stream=None):
+    """out[Nq,Hq,D] <- attention of the packed query rows q[Nq,Hq,D] (rows q_start[s]..q_start[s+1]-1 belong to
+    sequence s) to all context_lens[s] tokens of k/v_cache[NB,Hkv,B,D] through block_tables, without a mask.
+    lse[Nq,Hq] (fp32, optional) receives the natural log-sum-exp of the logits."""
+    import torch
+    Nq, Hq, D = q.shape
+    NB, Hkv, B, D2 = k_cache.shape
+    S = context_lens.shape[0]
+    if D2 != D or v_cache.shape != k_cache.shape or out.shape != q.shape:
+        raise ValueError("shape mismatch")
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or q_start.shape != (S + 1,):
+        raise ValueError("block_tables must be [S, max_blocks] and q_start [S + 1]")
+    if any(t.dtype != torch.int32 for t in (block_tables, context_lens, q_start)):
+        raise TypeError("block_tables, context_lens and q_start must be int32")
+    if not (out.dtype == q.dtype == k_cache.dtype == v_cache.dtype):
+        raise TypeError("q, out and the caches must share a dtype")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (Nq, Hq)):
+        raise ValueError("lse must be float32 [Nq, Hq]")
+    if workspace is None:
+        need = pa_cross_attention_workspace_size(S, Hq, Hkv, D, B, Nq, int(max_query_len), int(max_context_len))
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    st = lib.pa_cross_attention(_dev_ptr(out, "out"), None if lse is None else _dev_ptr(lse, "lse"), _dev_ptr(q, "q"),
+                                _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"),
+                                _dev_ptr(block_tables, "block_tables"), _dev_ptr(context_lens, "context_lens"),
+                                _dev_ptr(q_start, "q_start"), S, Hq, Hkv, D, B, block_tables.shape[1], NB, Nq,
+                                int(max_query_len), int(max_context_len), float(scale),
+                                _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+                                _dtype_code(q), _stream(stream))
+    _check(st, "pa_cross_attention")
+    return out
 
 
 def pa_swap_blocks(dst_k_cache, dst_v_cache, src_k_cache, src_v_cache, block_mapping, stream=None):

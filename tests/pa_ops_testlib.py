@@ -83,3 +83,11 @@ def logit_error(mags, D):
     """Bound of a logit's error in natural units: exact products (or one rounding each in fp32),
     D additions of fp32, the scale's and the maximum's subtraction's roundings."""
     return (2 * D + 8) * EPS32 * mags
+
+
+def output_tolerance(pr, v, out, mags, D):
+    """Bound of an output row's error when the weights are rounded once to bf16: that rounding (2^-8 of each
+    weight), the output's own, and the logits' errors in weights and sum."""
+    h = HALF[torch.bfloat16]
+    a = pr @ np.abs(v)
+    return h * a + h * np.abs(out) + a * (4 * logit_error(mags, D).max(initial=0.0) + 64 * EPS32) + 1e-30
