@@ -186,6 +186,42 @@ PA_API pa_status pa_decode_static_workspace(void* out, const void* q, const void
                                             int max_context_len, float scale, int partition_size,
                                             pa_dtype dtype, void* stream);
 
+/* ------------------------------------------------------------------ shared leading blocks */
+
+/* Bytes of device workspace pa_decode_shared needs.  0 on invalid arguments. */
+PA_API size_t pa_decode_shared_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                              int block_size, int max_context_len, int max_shared_len, int num_groups,
+                                              int num_group_rows);
+
+/*
+ * pa_decode for a batch in groups whose sequences share their leading blocks (a system
+ * prompt, the streams or beams of one prompt): the shared tokens are read once for all rows
+ * of a group instead of once per row.  The result is pa_decode's up to rounding (the weights
+ * of shared tokens are rounded to bf16 for their product with V).
+ *   group_rows    [num_group_rows] int32 (device): the batch rows of the groups, each row
+ *                 in one group at most; rows in no group attend on their own
+ *   group_start   [num_groups + 1] int32 (device): group g has the rows
+ *                 group_rows[group_start[g]] .. group_rows[group_start[g+1] - 1]
+ *   shared_lens   [num_groups] int32 (device): tokens that the rows of group g share, whole
+ *                 blocks, no more than any row's context.  The blocks are read through the
+ *                 first row's table; that the other rows' tables begin with the same ones is
+ *                 the caller's promise (pa_alloc_shared_groups finds such groups)
+ *   max_shared_len  host-side upper bound of shared_lens
+ *   workspace     device scratch of pa_decode_shared_workspace_size() bytes, 16-byte
+ *                 aligned; no initial contents.  Calls that share it must be ordered on one
+ *                 stream
+ * A group with a row out of range or listed twice, or with a bad shared length, raises
+ * PA_DEV_BAD_CONTEXT and is not shared (its rows attend on their own); starts that run
+ * backwards or leave [0, num_group_rows] do that for every group.  bf16, else as pa_decode.
+ */
+PA_API pa_status pa_decode_shared(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                  const int32_t* block_tables, const int32_t* context_lens, const int32_t* group_rows,
+                                  const int32_t* group_start, const int32_t* shared_lens, int num_seqs, int num_heads,
+                                  int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
+                                  int num_blocks, int num_groups, int num_group_rows, int max_context_len,
+                                  int max_shared_len, float scale, void* workspace, size_t workspace_bytes,
+                                  pa_dtype dtype, void* stream);
+
 /* ------------------------------------------------------------------ scores and eviction */
 
 /*
@@ -513,6 +549,18 @@ PA_API pa_status pa_alloc_append_slots(pa_allocator* a, const int64_t* seq_ids, 
 PA_API pa_status pa_alloc_beam_step(pa_allocator* a, const int64_t* beam_ids, int num_beams, const int32_t* parents,
                                     const int64_t* new_ids, int num_new, int64_t* slots_out, int64_t* cow_pairs_out,
                                     int* num_cow_out);
+
+/*
+ * Groups of the listed resident sequences (a batch, row i = seq_ids[i], all different) that
+ * share leading full blocks, for pa_decode_shared.  A row is in one group at most; of all
+ * groupings by common leading blocks this one saves the most block reads,
+ * sum over groups of (rows - 1) * shared blocks, with larger groups where two save the same.
+ * rows_out[n] receives the groups' rows (ascending within a group, groups by their first
+ * row), starts_out[n/2 + 1] and lens_out[n/2] the starts and the shared tokens (at most n/2
+ * groups: each has two rows or more), *num_groups_out their number.
+ */
+PA_API pa_status pa_alloc_shared_groups(const pa_allocator* a, const int64_t* seq_ids, int n, int32_t* rows_out,
+                                        int32_t* starts_out, int32_t* lens_out, int* num_groups_out);
 
 /*
  * Copy-on-write ahead of a change to the first num_tokens tokens of a resident sequence

@@ -29,6 +29,7 @@
 // zero is kept, unreferenced, for later prompts.  A block is taken from the free
 // queue first; when that is empty, the unreferenced cached block released longest
 // ago that has no cached children (a leaf) is evicted from the tree and reused.
+#include <algorithm>
 #include <cstdint>
 #include <cstring>
 #include <deque>
@@ -516,6 +517,97 @@ pa_status pa_alloc_beam_step(pa_allocator* a, const int64_t* beam_ids, int num_b
         }
     }
     *num_cow_out = ncow;
+    return PA_OK;
+}
+
+pa_status pa_alloc_shared_groups(const pa_allocator* a, const int64_t* seq_ids, int n, int32_t* rows_out,
+                                 int32_t* starts_out, int32_t* lens_out, int* num_groups_out)
+{
+    if (!a || n < 0 || !num_groups_out || !starts_out || (n > 0 && (!seq_ids || !rows_out || !lens_out))) {
+        pa::set_error("pa_alloc_shared_groups: bad argument");
+        return PA_ERR_INVALID;
+    }
+    struct Row {
+        const int32_t* t;  // full blocks
+        int32_t len, row;
+    };
+    std::vector<Row> v((size_t)n);
+    for (int i = 0; i < n; ++i) {
+        auto it = a->seqs.find(seq_ids[i]);
+        if (it == a->seqs.end() || it->second.on_host) {
+            pa::set_error("pa_alloc_shared_groups: unknown or swapped-out sequence");
+            return PA_ERR_INVALID;
+        }
+        v[(size_t)i] = Row{it->second.table.data(), (int32_t)(it->second.tokens / a->block_size), i};
+    }
+    // Sorted by table, the rows that share d leading blocks are neighbours whose common lengths are d or
+    // more: the intervals of the common-length array, nested like the prefixes themselves.
+    std::sort(v.begin(), v.end(), [](const Row& x, const Row& y) {
+        const int32_t m = std::min(x.len, y.len);
+        for (int32_t k = 0; k < m; ++k)
+            if (x.t[k] != y.t[k]) return x.t[k] < y.t[k];
+        return x.len != y.len ? x.len < y.len : x.row < y.row;
+    });
+    struct Group {
+        int left, right;  // rows v[left .. right]
+        int32_t blocks;
+    };
+    struct Open {
+        int32_t blocks;
+        int left;
+        size_t first;     // groups chosen inside it start here
+        int64_t saved;    // what they save
+    };
+    std::vector<Group> chosen;
+    std::vector<Open> open;
+    for (int i = 1; i <= n; ++i) {
+        int32_t lcp = 0;
+        if (i < n) {
+            const Row &x = v[(size_t)i - 1], &y = v[(size_t)i];
+            const int32_t m = std::min(x.len, y.len);
+            while (lcp < m && x.t[lcp] == y.t[lcp]) ++lcp;
+        }
+        int left = i - 1;
+        size_t first = chosen.size();
+        int64_t saved = 0;
+        while (!open.empty() && open.back().blocks > lcp) {
+            Open o = open.back();
+            open.pop_back();
+            o.saved += saved;
+            const int64_t whole = (int64_t)(i - 1 - o.left) * o.blocks;
+            if (whole >= o.saved) {  // one group for the interval, in place of those inside it
+                chosen.resize(o.first);
+                chosen.push_back(Group{o.left, i - 1, o.blocks});
+                o.saved = whole;
+            }
+            left = o.left;
+            first = o.first;
+            saved = o.saved;
+        }
+        if (lcp > 0) {
+            if (!open.empty() && open.back().blocks == lcp)
+                open.back().saved += saved;
+            else
+                open.push_back(Open{lcp, left, first, saved});
+        }
+    }
+    std::vector<std::vector<int32_t>> rows;
+    for (const Group& g : chosen) {
+        std::vector<int32_t> r;
+        for (int k = g.left; k <= g.right; ++k) r.push_back(v[(size_t)k].row);
+        std::sort(r.begin(), r.end());
+        r.push_back(g.blocks);
+        rows.push_back(std::move(r));
+    }
+    std::sort(rows.begin(), rows.end());  // by first row
+    int at = 0, ng = 0;
+    starts_out[0] = 0;
+    for (const auto& r : rows) {
+        for (size_t k = 0; k + 1 < r.size(); ++k) rows_out[at++] = r[k];
+        lens_out[ng] = r.back() * a->block_size;
+        starts_out[++ng] = at;
+    }
+    *num_groups_out = ng;
     return PA_OK;
 }
 

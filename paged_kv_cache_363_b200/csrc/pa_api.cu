@@ -15,6 +15,7 @@
 #include "pa.h"
 #include "pa_group.cuh"
 #include "pa_internal.h"
+#include "pa_shared.h"
 
 namespace pa {
 
@@ -695,8 +696,8 @@ pa_status pa_cross_attention(void* out, float* lse, const void* q, const void* k
     }
     const CrossWorkspace w = cross_workspace((size_t)num_seqs, (size_t)num_heads, num_kv_heads, head_dim,
                                              (size_t)num_query_tokens, max_query_len, max_context_len);
-    if (w.entries * (size_t)num_kv_heads > (size_t)INT32_MAX) {
-        set_error("pa_cross_attention: too many query tiles");
+    if (w.entries * (size_t)num_kv_heads > (size_t)INT32_MAX || w.merges * (size_t)num_heads > (size_t)INT32_MAX) {
+        set_error("pa_cross_attention: too many query rows");
         return PA_ERR_UNSUPPORTED;
     }
     if (!workspace || workspace_bytes < w.total || !aligned(workspace, 16)) {
@@ -740,6 +741,132 @@ pa_status pa_cross_attention(void* out, float* lse, const void* q, const void* k
     a.max_chunks = w.chunks;
     const cudaError_t e = launch_cross(a, head_dim, num_heads / num_kv_heads, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail("pa_cross_attention launch", e);
+    return PA_OK;
+}
+
+size_t pa_decode_shared_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                       int max_context_len, int max_shared_len, int num_groups, int num_group_rows)
+{
+    if (num_seqs <= 0 || max_context_len < 0 || max_shared_len < 0 || num_groups < 0 || num_group_rows < 0 ||
+        check_common("pa_decode_shared_workspace_size", num_kv_heads, head_dim, block_size, 1, PA_DTYPE_BF16) != PA_OK ||
+        check_group("pa_decode_shared_workspace_size", num_heads, num_kv_heads, 1, block_size, PA_DTYPE_BF16) != PA_OK)
+        return 0;
+    return shared_workspace((size_t)num_seqs, (size_t)num_heads, num_kv_heads, head_dim, max_context_len, max_shared_len,
+                            (size_t)num_groups, (size_t)num_group_rows)
+        .total;
+}
+
+pa_status pa_decode_shared(void* out, const void* q, const void* k_cache, const void* v_cache,
+                           const int32_t* block_tables, const int32_t* context_lens, const int32_t* group_rows,
+                           const int32_t* group_start, const int32_t* shared_lens, int num_seqs, int num_heads,
+                           int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq, int num_blocks,
+                           int num_groups, int num_group_rows, int max_context_len, int max_shared_len, float scale,
+                           void* workspace, size_t workspace_bytes, pa_dtype dtype, void* stream)
+{
+    pa::CallRange range("pa_decode_shared");
+    pa_status st = check_common("pa_decode_shared", num_kv_heads, head_dim, block_size, num_blocks, dtype);
+    if (st != PA_OK) return st;
+    st = check_group("pa_decode_shared", num_heads, num_kv_heads, num_blocks, block_size, dtype);
+    if (st != PA_OK) return st;
+    if (num_seqs < 0 || num_seqs > 65535 || max_blocks_per_seq <= 0 || max_context_len < 0 || max_shared_len < 0 ||
+        num_groups < 0 || num_groups > 65535 || num_group_rows < 0 || num_group_rows > num_seqs ||
+        !std::isfinite(scale)) {
+        set_error("pa_decode_shared: bad size or scale (a row is in one group at most)");
+        return PA_ERR_INVALID;
+    }
+    if ((max_context_len + (int64_t)kMaxPartitionTokens - 1) / kMaxPartitionTokens > kMaxPartitions) {
+        set_error("pa_decode_shared: max_context_len exceeds " + std::to_string(kMaxPartitions) + " partitions of " +
+                  std::to_string(kMaxPartitionTokens) + " tokens");
+        return PA_ERR_UNSUPPORTED;
+    }
+    if (num_seqs == 0) return PA_OK;
+    if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens ||
+        (num_groups > 0 && (!group_start || !shared_lens)) || (num_group_rows > 0 && !group_rows)) {
+        set_error("pa_decode_shared: null pointer");
+        return PA_ERR_INVALID;
+    }
+    if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(group_rows, 4) || !aligned(group_start, 4) ||
+        !aligned(shared_lens, 4)) {
+        set_error("pa_decode_shared: misaligned pointer (q, out, caches need 16 bytes)");
+        return PA_ERR_INVALID;
+    }
+    const SharedWorkspace w =
+        shared_workspace((size_t)num_seqs, (size_t)num_heads, num_kv_heads, head_dim, max_context_len, max_shared_len,
+                         (size_t)num_groups, (size_t)num_group_rows);
+    if (std::max(w.entries, (size_t)num_seqs * (size_t)w.parts) * (size_t)num_kv_heads > (size_t)INT32_MAX ||
+        (size_t)num_seqs * (size_t)num_heads > (size_t)INT32_MAX) {
+        set_error("pa_decode_shared: too many rows");
+        return PA_ERR_UNSUPPORTED;
+    }
+    if (!workspace || workspace_bytes < w.total || !aligned(workspace, 16)) {
+        set_error("pa_decode_shared: workspace missing, too small (need " + std::to_string(w.total) +
+                  " bytes) or not 16-byte aligned");
+        return PA_ERR_INVALID;
+    }
+    unsigned int* status = nullptr;
+    st = status_ptr(&status);
+    if (st != PA_OK) return st;
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    SharedArgs a{};
+    a.g.out = out;
+    a.g.q = q;
+    a.g.k_cache = k_cache;
+    a.g.v_cache = v_cache;
+    a.g.block_tables = block_tables;
+    a.g.rows = group_rows;
+    a.g.items = reinterpret_cast<const GroupItem*>(ws + w.g.items);
+    a.g.counts = reinterpret_cast<const unsigned*>(ws + w.g.header);
+    a.g.merge_list = reinterpret_cast<const uint2*>(ws + w.g.merges);
+    a.g.ws_acc = reinterpret_cast<float*>(ws + w.acc);
+    a.g.ws_ml = reinterpret_cast<float*>(ws + w.ml);
+    a.g.status = status;
+    a.g.num_heads = num_heads;
+    a.g.num_kv_heads = num_kv_heads;
+    a.g.max_blocks_per_seq = max_blocks_per_seq;
+    a.g.num_blocks = num_blocks;
+    a.g.block_size = block_size;
+    a.g.num_partitions = w.chunks + w.parts;
+    a.g.lead_partitions = w.chunks;
+    a.g.max_entries = num_groups > 0 ? (int)w.entries : 0;
+    a.g.max_merges = num_seqs;
+    a.g.scale_log2 = scale * 1.4426950408889634f;
+    a.d.out = out;
+    a.d.q = q;
+    a.d.k_cache = k_cache;
+    a.d.v_cache = v_cache;
+    a.d.block_tables = block_tables;
+    a.d.context_lens = context_lens;
+    a.d.plan = reinterpret_cast<unsigned*>(ws + w.plan);
+    a.d.plan_list = reinterpret_cast<uint2*>(ws + w.list);
+    a.d.ws_acc = reinterpret_cast<float*>(ws + w.acc);
+    a.d.ws_ml = reinterpret_cast<float*>(ws + w.ml);
+    a.d.status = status;
+    a.d.num_seqs = num_seqs;
+    a.d.num_heads = num_heads;
+    a.d.num_kv_heads = num_kv_heads;
+    a.d.max_blocks_per_seq = max_blocks_per_seq;
+    a.d.num_blocks = num_blocks;
+    a.d.max_context_len = max_context_len;
+    a.d.partition_blocks = shared_partition(max_context_len) / block_size;
+    a.d.adaptive = 1;
+    a.d.num_partitions = w.chunks + w.parts;
+    a.d.lead_partitions = w.chunks;
+    a.d.scale_log2 = a.g.scale_log2;
+    a.group_rows = group_rows;
+    a.group_start = group_start;
+    a.shared_lens = shared_lens;
+    a.listed = reinterpret_cast<int*>(ws + w.listed);
+    a.lead_blocks = reinterpret_cast<int*>(ws + w.lead_blocks);
+    a.lead_states = reinterpret_cast<int*>(ws + w.lead_states);
+    a.group_ok = reinterpret_cast<int*>(ws + w.group_ok);
+    a.num_groups = num_groups;
+    a.num_group_rows = num_group_rows;
+    a.max_shared_len = max_shared_len;
+    a.max_chunks = w.chunks;
+    const cudaError_t e =
+        launch_shared(a, head_dim, block_size, num_heads / num_kv_heads, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail("pa_decode_shared launch", e);
     return PA_OK;
 }
 

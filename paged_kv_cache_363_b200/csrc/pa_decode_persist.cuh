@@ -151,8 +151,9 @@ __global__ void __launch_bounds__(Persist<Cons, BS>::THREADS, 2)
     // only its unit producer waits for the plan, before its second unit.  Every other
     // CTA waits here; the plan kernel's list and counters are visible after the wait.
     const bool early = (int)blockIdx.x < a.first_wave;
-    // (kModeOwn: the kernel before this one starts it only after it has waited for the plan.)
-    if (MODE != kModeOwn && !early) pdl_wait_primary();
+    // (kModeOwn: the kernel before this one starts it only after it has waited for the plan,
+    // unless that kernel is the plan.)
+    if (MODE == kModeOwn ? a.wait_first != 0 : !early) pdl_wait_primary();
 
     auto slot = [&](int k) { return smem + P::OFF_SLOT + (k % UR) * P::SLOT_BYTES; };
     auto slot_table = [&](int k) { return reinterpret_cast<int*>(slot(k) + P::QBYTES); };

@@ -40,6 +40,8 @@ SIGNATURES = [
     ("pa_decode_plan", _int, [_vp, _vp] + [_int] * 9 + [_vp, _sz, _int, _vp]),
     ("pa_decode_run", _int, [_vp, _vp, _vp, _vp, _vp, _vp] + [_int] * 8 + [_f32, _int, _vp, _sz, _int, _vp]),
     ("pa_decode_static_workspace", _int, [_vp, _vp, _vp, _vp, _vp, _vp] + [_int] * 8 + [_f32, _int, _int, _vp]),
+    ("pa_decode_shared_workspace_size", _sz, [_int] * 9),
+    ("pa_decode_shared", _int, [_vp] * 9 + [_int] * 11 + [_f32, _vp, _sz, _int, _vp]),
     ("pa_decode_scores_workspace_size", _sz, [_int] * 7),
     ("pa_decode_scores", _int, [_vp] * 7 + [_int] * 9 + [_f32, _int, _vp, _sz, _int, _vp]),
     ("pa_evict_workspace_size", _sz, [_int] * 3),
@@ -64,6 +66,7 @@ SIGNATURES = [
     ("pa_alloc_append_slot", _int, [_vp, _i64, ctypes.POINTER(_i64), ctypes.POINTER(_i32), ctypes.POINTER(_i32)]),
     ("pa_alloc_append_slots", _int, [_vp, _vp, _int, _vp, _vp, ctypes.POINTER(_int)]),
     ("pa_alloc_beam_step", _int, [_vp, _vp, _int, _vp, _vp, _int, _vp, _vp, ctypes.POINTER(_int)]),
+    ("pa_alloc_shared_groups", _int, [_vp, _vp, _int, _vp, _vp, _vp, ctypes.POINTER(_int)]),
     ("pa_alloc_make_private", _int, [_vp, _i64, _int, _vp, ctypes.POINTER(_int)]),
     ("pa_alloc_truncate", _int, [_vp, _i64, _int]),
     ("pa_alloc_free_seq", _int, [_vp, _i64]),
@@ -236,6 +239,45 @@ def pa_decode_static_workspace(out, q, k_cache, v_cache, block_tables, context_l
                                         block_tables.shape[1], NB, int(max_context_len), float(scale),
                                         int(partition_size), dt, _stream(stream))
     _check(st, "pa_decode_static_workspace")
+    return out
+
+
+def pa_decode_shared_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len,
+                                    max_shared_len, num_groups, num_group_rows):
+    return int(lib.pa_decode_shared_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, block_size,
+                                                   max_context_len, max_shared_len, num_groups, num_group_rows))
+
+
+def pa_decode_shared(out, q, k_cache, v_cache, block_tables, context_lens, group_rows, group_start, shared_lens,
+                     max_context_len, max_shared_len, scale, workspace=None, stream=None):
+    """pa_decode of a batch in groups that share leading blocks, read once per group: group g has the batch rows
+    group_rows[group_start[g]:group_start[g+1]] and shares shared_lens[g] tokens (whole blocks).  See
+    Allocator.shared_groups."""
+    import torch
+    S, Hq, D = q.shape
+    NB, Hkv, B, D2 = k_cache.shape
+    n, groups = group_rows.shape[0], shared_lens.shape[0]
+    if D2 != D or v_cache.shape != k_cache.shape or out.shape != q.shape:
+        raise ValueError("shape mismatch")
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,):
+        raise ValueError("block_tables must be [S, max_blocks] and context_lens [S]")
+    if group_rows.dim() != 1 or shared_lens.dim() != 1 or group_start.shape != (groups + 1,):
+        raise ValueError("group_rows must be [rows], shared_lens [groups] and group_start [groups + 1]")
+    if any(t.dtype != torch.int32 for t in (block_tables, context_lens, group_rows, group_start, shared_lens)):
+        raise TypeError("tables, context lengths, rows, starts and shared lengths must be int32")
+    if not (out.dtype == q.dtype == k_cache.dtype == v_cache.dtype):
+        raise TypeError("q, out and the caches must share a dtype")
+    if workspace is None:
+        need = pa_decode_shared_workspace_size(S, Hq, Hkv, D, B, int(max_context_len), int(max_shared_len), groups, n)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    st = lib.pa_decode_shared(_dev_ptr(out, "out"), _dev_ptr(q, "q"), _dev_ptr(k_cache, "k_cache"),
+                              _dev_ptr(v_cache, "v_cache"), _dev_ptr(block_tables, "block_tables"),
+                              _dev_ptr(context_lens, "context_lens"), _dev_ptr(group_rows, "group_rows"),
+                              _dev_ptr(group_start, "group_start"), _dev_ptr(shared_lens, "shared_lens"), S, Hq, Hkv, D,
+                              B, block_tables.shape[1], NB, groups, n, int(max_context_len), int(max_shared_len),
+                              float(scale), _dev_ptr(workspace, "workspace"),
+                              workspace.numel() * workspace.element_size(), _dtype_code(q), _stream(stream))
+    _check(st, "pa_decode_shared")
     return out
 
 
@@ -563,6 +605,18 @@ class Allocator:
         _check(lib.pa_alloc_beam_step(self._h, _np_ptr(old), old.shape[0], _np_ptr(par), _np_ptr(new), n,
                                       _np_ptr(slots), _np_ptr(pairs), ctypes.byref(ncow)), "pa_alloc_beam_step")
         return slots[:n], pairs[:ncow.value]
+
+    def shared_groups(self, seq_ids):
+        """Groups of the batch's rows that share leading full blocks, for pa_decode_shared: (group_rows,
+        group_start, shared_lens) as int32 arrays."""
+        ids = np.ascontiguousarray(seq_ids, dtype=np.int64)
+        n = ids.shape[0]
+        rows, starts, lens = np.empty(max(1, n), np.int32), np.empty(n // 2 + 1, np.int32), np.empty(n // 2 + 1, np.int32)
+        ng = _int(0)
+        _check(lib.pa_alloc_shared_groups(self._h, _np_ptr(ids), n, _np_ptr(rows), _np_ptr(starts), _np_ptr(lens),
+                                          ctypes.byref(ng)), "pa_alloc_shared_groups")
+        g = ng.value
+        return rows[:starts[g]], starts[:g + 1], lens[:g]
 
     def make_private(self, seq_id, num_tokens):
         """Replaces the shared or cached blocks of the first num_tokens tokens by fresh ones; returns the

@@ -26,7 +26,33 @@ def _round_up(x, m):
     return (x + m - 1) // m * m
 
 
-class DecodeBatch:
+class SharedDecode:
+    """Decode of a batch whose sequences share leading blocks, each shared block read once per group."""
+
+    def shared_groups(self):
+        """The allocator's groups for this step's rows, on the device: (rows, starts, shared lengths), and the
+        longest shared length."""
+        if getattr(self, "_groups", None) is None:
+            g = self.alloc.shared_groups(np.arange(self.wl.num_seqs, dtype=np.int64))
+            self._groups = tuple(torch.from_numpy(x.copy()).to(self.device) for x in g), int(g[2].max(initial=0))
+        return self._groups
+
+    def decode_shared(self, out=None, stream=None):
+        """The step's decode through pa_decode_shared (bf16)."""
+        out = self.out if out is None else out
+        wl = self.wl
+        (rows, starts, lens), longest = self.shared_groups()
+        need = pa.pa_decode_shared_workspace_size(wl.num_seqs, wl.num_heads, wl.num_kv_heads, wl.head_dim,
+                                                  wl.block_size, self.max_context_len, longest, lens.shape[0],
+                                                  rows.shape[0])
+        if getattr(self, "shared_workspace", None) is None:
+            self.shared_workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=self.device)
+        return pa.pa_decode_shared(out, self.q, self.k_cache, self.v_cache, self.block_tables, self.context_lens, rows,
+                                   starts, lens, self.max_context_len, longest, wl.scale,
+                                   workspace=self.shared_workspace, stream=stream)
+
+
+class DecodeBatch(SharedDecode):
     def __init__(self, wl, device="cuda", values=None, fill=float("nan"), partition_size=None):
         self.wl = wl
         self.device = torch.device(device)
@@ -126,7 +152,7 @@ class DecodeBatch:
         return wl.num_seqs * (2 * row * 2 + 8)
 
 
-class CowBatch:
+class CowBatch(SharedDecode):
     """Parallel sampling: prompts forked into streams, then private appends with copy-on-write."""
 
     def __init__(self, wl, device="cuda", values=None, fill=float("nan"), partition_size=None):
@@ -218,7 +244,7 @@ class CowBatch:
         return wl.num_seqs * (2 * wl.num_kv_heads * wl.head_dim * 2 * 2 + 8)
 
 
-class PrefixBatch:
+class PrefixBatch(SharedDecode):
     """Requests sharing system prompts through the allocator's prefix cache.
 
     Each request's prompt (all its tokens but the last) is added by token ids; only
@@ -303,7 +329,7 @@ class PrefixBatch:
     append_bytes = DecodeBatch.append_bytes
 
 
-class BeamBatch:
+class BeamBatch(SharedDecode):
     """Beam search through the allocator's beam step.
 
     Each request's prompt is written once and forked into its beams.  Every beam step

@@ -60,6 +60,123 @@ def test_evict_nothing_to_do_and_workspace():
     assert pa.pa_evict_workspace_size(0, 4, 10) == 0
 
 
+def _cross(out=P, lse=None, q=P, S=1, Hq=4, Hkv=4, D=128, B=16, mb=4, NB=8, Nq=5, mq=5, ctx=64, scale=1.0, ws=P,
+           nbytes=1 << 30, dt=1):
+    return pa.lib.pa_cross_attention(out, lse, q, P, P, P, P, P, S, Hq, Hkv, D, B, mb, NB, Nq, mq, ctx, scale, ws, nbytes, dt,
+                                     None)
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(D=96), "UNSUPPORTED"), (dict(B=8), "UNSUPPORTED"), (dict(dt=0), "UNSUPPORTED"), (dict(Hq=12), "UNSUPPORTED"),
+    (dict(Hq=6), "INVALID"), (dict(Hq=0), "INVALID"), (dict(q=ODD), "INVALID"), (dict(out=None), "INVALID"),
+    (dict(lse=ctypes.c_void_p(0x1002)), "INVALID"), (dict(scale=float("inf")), "INVALID"), (dict(ws=None), "INVALID"),
+    (dict(nbytes=64), "INVALID"), (dict(S=65536), "INVALID"), (dict(ctx=-1), "INVALID"), (dict(mq=-1), "INVALID"),
+    (dict(NB=1 << 26), "UNSUPPORTED"), (dict(Nq=2 ** 31 - 1, Hq=128, Hkv=16), "UNSUPPORTED")])
+def test_cross_attention_refusals(bad, code):
+    assert _cross(**bad) == getattr(pa, "PA_ERR_" + code)
+    assert "pa_cross_attention" in pa.lib.pa_last_error_string().decode()
+
+
+def test_cross_attention_nothing_to_do_and_workspace():
+    for none in (dict(S=0), dict(Nq=0), dict(mq=0)):
+        assert _cross(out=None, q=None, ws=None, **none) == pa.PA_OK
+    # without partial states: entries alone; with few rows and a long context, 32 states per (row, head) at most
+    many = pa.pa_cross_attention_workspace_size(4, 32, 8, 128, 16, 100000, 50000, 1 << 20)
+    assert 0 < many < 100000 * 32
+    few = pa.pa_cross_attention_workspace_size(1, 8, 1, 128, 16, 1, 1, 1 << 20)
+    assert 32 * 8 * (128 + 2) * 4 <= few <= 2 * 32 * 8 * (128 + 2) * 4
+    assert pa.pa_cross_attention_workspace_size(1, 12, 4, 128, 16, 1, 1, 64) == 0
+
+
+def _shared(out=P, q=P, rows=P, start=P, lens=P, S=8, Hq=4, Hkv=4, D=128, B=16, mb=4, NB=8, ng=2, nr=6, ctx=64, sh=32,
+            scale=1.0, ws=P, nbytes=1 << 30, dt=1):
+    return pa.lib.pa_decode_shared(out, q, P, P, P, P, rows, start, lens, S, Hq, Hkv, D, B, mb, NB, ng, nr, ctx, sh, scale, ws,
+                                   nbytes, dt, None)
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(D=96), "UNSUPPORTED"), (dict(B=8), "UNSUPPORTED"), (dict(dt=0), "UNSUPPORTED"), (dict(Hq=12), "UNSUPPORTED"),
+    (dict(Hq=6), "INVALID"), (dict(nr=9), "INVALID"), (dict(ng=-1), "INVALID"), (dict(sh=-1), "INVALID"),
+    (dict(rows=None), "INVALID"), (dict(start=None), "INVALID"), (dict(lens=None), "INVALID"), (dict(q=ODD), "INVALID"),
+    (dict(scale=float("nan")), "INVALID"), (dict(ws=None), "INVALID"), (dict(nbytes=64), "INVALID"),
+    (dict(S=65536), "INVALID"), (dict(mb=0), "INVALID"), (dict(NB=1 << 26), "UNSUPPORTED"),
+    (dict(ctx=2048 * 4096 + 1), "UNSUPPORTED")])
+def test_decode_shared_refusals(bad, code):
+    assert _shared(**bad) == getattr(pa, "PA_ERR_" + code)
+    assert "pa_decode_shared" in pa.lib.pa_last_error_string().decode()
+
+
+def test_decode_shared_nothing_to_do_and_workspace():
+    assert _shared(S=0, nr=0, out=None, q=None, ws=None) == pa.PA_OK
+    # a partial state per chunk and per partition, for every row and head; no groups need no chunks
+    w = pa.pa_decode_shared_workspace_size(8, 32, 8, 128, 16, 1000, 512, 2, 8)
+    assert w >= 8 * 32 * (2 + 2) * 130 * 4
+    assert 0 < pa.pa_decode_shared_workspace_size(8, 32, 8, 128, 16, 1000, 0, 0, 0) < w
+    assert pa.pa_decode_shared_workspace_size(8, 32, 8, 128, 16, 1000, -1, 0, 0) == 0
+
+
+def _best_saving(tables):
+    """The most block reads any grouping of rows by common leading blocks saves, by recursion over prefixes."""
+    if len(tables) < 2:
+        return 0
+    d = 0
+    while all(len(t) > d and t[d] == tables[0][d] for t in tables):
+        d += 1
+    parts = {}
+    for t in tables:
+        if len(t) > d:
+            parts.setdefault(t[d], []).append(t)
+    return max((len(tables) - 1) * d, sum(_best_saving(p) for p in parts.values()))
+
+
+@pytest.mark.parametrize("seed", range(20))
+def test_shared_groups_save_the_most(seed):
+    rng = np.random.default_rng(seed)
+    B = int(rng.choice([2, 4]))
+    a = pa.Allocator(3000, B, rng.permutation(3000).astype(np.int32))
+    stems = [rng.integers(0, 3, size=40).tolist() for _ in range(3)]
+    n = int(rng.integers(1, 40))
+    for i in range(n):
+        kind = rng.integers(4)
+        if kind == 0 or i == 0:
+            a.add_seq(i, int(rng.integers(0, 5 * B)))
+        elif kind == 1:
+            a.fork(int(rng.integers(i)), i)
+        else:
+            s = stems[rng.integers(3)]
+            a.add_seq_cached(i, s[:int(rng.integers(1, 40))] + rng.integers(3, 9, size=5).tolist())
+        for _ in range(int(rng.integers(0, 4))):
+            a.append_slot(i)
+    ids = rng.permutation(n)[:max(1, n - 2)]
+    rows, starts, lens = a.shared_groups(ids)
+    full = [a.block_table(int(s))[:a.num_tokens(int(s)) // B] for s in ids]
+    assert len(set(rows.tolist())) == len(rows) and starts[0] == 0 and starts[-1] == len(rows)
+    saved, firsts = 0, []
+    for g, L in enumerate(lens):
+        r = rows[starts[g]:starts[g + 1]]
+        assert len(r) >= 2 and L > 0 and L % B == 0 and r.tolist() == sorted(r.tolist())
+        assert len({tuple(full[i][:L // B]) for i in r}) == 1 and all(len(full[i]) >= L // B for i in r)
+        saved += (len(r) - 1) * (L // B)
+        firsts.append(r[0])
+    assert firsts == sorted(firsts)
+    assert saved == _best_saving(full)
+
+
+def test_shared_groups_of_none_and_of_swapped_sequences():
+    a = pa.Allocator(8, 4)
+    rows, starts, lens = a.shared_groups([])
+    assert (len(rows), starts.tolist(), len(lens)) == (0, [0], 0)
+    a.add_host_pool(4)
+    a.add_seq(0, 8)
+    a.fork(0, 1)
+    assert a.shared_groups([1, 0])[2].tolist() == [8]
+    a.swap_out(1)
+    with pytest.raises(pa.PAError):
+        a.shared_groups([1, 0])
+    with pytest.raises(pa.PAError):
+        a.shared_groups([5])
+
+
 def _same(lib_a, ora, NB):
     assert lib_a.num_free() == ora.num_free() and lib_a.num_cached_free() == ora.num_cached_free()
     assert [lib_a.ref_count(b) for b in range(NB)] == ora.ref
