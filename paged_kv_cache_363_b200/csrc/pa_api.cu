@@ -617,7 +617,7 @@ CrossWorkspace cross_workspace(size_t S, size_t Hq, int Hkv, int D, size_t Nq, i
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     CrossWorkspace w{};
     const int G = (int)(Hq / (size_t)Hkv);
-    const size_t T = 128 / (size_t)G;
+    const size_t T = ((int64_t)max_query_len * G <= 64 ? 64 : 128) / (size_t)G;
     w.chunks = group_max_chunks(max_context_len, (int64_t)Nq, G, Hkv);
     w.entries = (S + Nq / T) * (size_t)w.chunks;
     w.merges = w.chunks > 1 ? Nq : 0;
@@ -817,7 +817,6 @@ pa_status pa_decode_shared(void* out, const void* q, const void* k_cache, const 
     a.g.rows = group_rows;
     a.g.items = reinterpret_cast<const GroupItem*>(ws + w.g.items);
     a.g.counts = reinterpret_cast<const unsigned*>(ws + w.g.header);
-    a.g.merge_list = reinterpret_cast<const uint2*>(ws + w.g.merges);
     a.g.ws_acc = reinterpret_cast<float*>(ws + w.acc);
     a.g.ws_ml = reinterpret_cast<float*>(ws + w.ml);
     a.g.status = status;
@@ -829,7 +828,6 @@ pa_status pa_decode_shared(void* out, const void* q, const void* k_cache, const 
     a.g.num_partitions = w.chunks + w.parts;
     a.g.lead_partitions = w.chunks;
     a.g.max_entries = num_groups > 0 ? (int)w.entries : 0;
-    a.g.max_merges = num_seqs;
     a.g.scale_log2 = scale * 1.4426950408889634f;
     a.d.out = out;
     a.d.q = q;
@@ -856,7 +854,9 @@ pa_status pa_decode_shared(void* out, const void* q, const void* k_cache, const 
     a.group_rows = group_rows;
     a.group_start = group_start;
     a.shared_lens = shared_lens;
+    a.row_info = ws + w.row_info;
     a.listed = reinterpret_cast<int*>(ws + w.listed);
+    a.ctx = reinterpret_cast<int*>(ws + w.ctx);
     a.lead_blocks = reinterpret_cast<int*>(ws + w.lead_blocks);
     a.lead_states = reinterpret_cast<int*>(ws + w.lead_states);
     a.group_ok = reinterpret_cast<int*>(ws + w.group_ok);

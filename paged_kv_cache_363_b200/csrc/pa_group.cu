@@ -14,9 +14,9 @@
 // at D = 128) takes 0.74 us at a 148th of the measured copy rate, its two products 0.27 us.
 //
 // A CTA runs units (entry, kv head) b, b + grid, ...; two CTAs per SM, each with
-//   - warp 4: K and V by TMA, one 16-row box per (16-token run of a block, 64 columns),
-//     128-byte swizzle, rings of ST stages that run on across units;
-//   - warp 5 (one thread): S = Q K^T (M = 128, N = 64) into one of two tensor-memory buffers
+//   - warps 4 and 5: K and V by TMA, one 16-row box per (16-token run of a block, 64
+//     columns), 128-byte swizzle, rings of ST stages that run on across units;
+//   - warp 6 (one thread): S = Q K^T (M = 128, N = 64) into one of two tensor-memory buffers
 //     and O += P V (A = P from tensor memory, V MN-major); S of the next tile is issued before
 //     P V of this one, so the tensor core works while the softmax does;
 //   - warps 0-3: the softmax, a thread per row, which also fetch the rows of Q (cp.async,
@@ -45,30 +45,38 @@
 namespace pa {
 namespace {
 
-constexpr int kRows = 128;      // rows of a tile
+constexpr int kRows = 128;      // rows of an MMA tile
 constexpr int kTok = 64;        // tokens per K/V tile
 constexpr int kBox = 16;        // rows per TMA box
 constexpr int kNBox = kTok / kBox;
-constexpr int kThreads = 192;   // 4 softmax warps, producer, MMA issuer
-constexpr int kProdWarp = 4, kMmaWarp = 5;
+constexpr int kThreads = 224;   // 4 softmax warps, producers of K and of V, MMA issuer
+constexpr int kKWarp = 4, kVWarp = 5, kMmaWarp = 6;
 constexpr uint32_t kTmemCols = 256;  // S 0..63 and 64..127 (P over their first 32), O 128..
 constexpr float kLazy = 8.f;    // base-2 units
 
-template <int D>
+// QR: the rows of Q kept in shared memory (a unit's most).  The MMA always takes 128 rows: those past QR
+// are whatever lies behind Q (the K stages), give rows of S and O that nobody reads, and leave 16 KB more
+// for K and V where few rows share them.
+template <int D, int QR>
 struct Cfg {
     static constexpr int NH = D / 64;             // 64-column halves
-    static constexpr int QHALF = kRows * 128;     // bytes of a half of Q
+    static constexpr int QHALF = QR * 128;        // bytes of a half of Q
     static constexpr int KVHALF = kTok * 128;     // bytes of a half of a K or V tile
     static constexpr int TILE = NH * KVHALF;
-    static constexpr int ST = D == 128 ? 2 : 4;   // stages of K and of V: 64 KB together either way
+    static constexpr int ST = (D == 128 ? 1 : 2) * (QR == 64 ? 3 : 2);  // stages of K and of V
     static constexpr int OFF_K = NH * QHALF;
     static constexpr int OFF_V = OFF_K + ST * TILE;
     static constexpr int OFF_BAR = OFF_V + ST * TILE;
     static constexpr int NBAR = 4 * ST + 8;       // k_full, k_empty, v_full, v_empty [ST], q_full, s_full[2], p_full[2],
                                                   // o_done, o_free, drain
-    static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
+    static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16;
 };
-static_assert(2 * (Cfg<128>::SMEM + 1024) <= 227 * 1024, "two CTAs per SM");
+static_assert(2 * (Cfg<128, 64>::SMEM + 1024) <= 227 * 1024 && 2 * (Cfg<128, 128>::SMEM + 1024) <= 227 * 1024 &&
+                  2 * (Cfg<64, 64>::SMEM + 1024) <= 227 * 1024 && 2 * (Cfg<64, 128>::SMEM + 1024) <= 227 * 1024,
+              "two CTAs per SM");
+static_assert(Cfg<64, 64>::OFF_K + Cfg<64, 64>::ST * Cfg<64, 64>::TILE >= 128 * 128 &&
+                  Cfg<128, 64>::OFF_K + Cfg<128, 64>::ST * Cfg<128, 64>::TILE >= Cfg<128, 64>::QHALF + 128 * 128,
+              "128 rows from either half of Q lie inside the tiles");
 
 __device__ __forceinline__ float ex2(float x)
 {
@@ -107,8 +115,11 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src)
 
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-__device__ __forceinline__ GroupItem load_item(const GroupArgs& a, unsigned unit)
+// The entry of a unit, or an empty one past the end.  Every role asks for a unit's entry a whole unit before
+// it needs it, so that no trip to memory stands between two units.
+__device__ __forceinline__ GroupItem load_item(const GroupArgs& a, unsigned unit, unsigned nunits)
 {
+    if (unit >= nunits) return GroupItem{0, 0, 0, 0, 0, 0, {0, 0}};
     const int4* p = reinterpret_cast<const int4*>(a.items + unit / (unsigned)a.num_kv_heads);
     const int4 x = __ldcg(p), y = __ldcg(p + 1);
     GroupItem it;
@@ -121,15 +132,19 @@ __device__ __forceinline__ GroupItem load_item(const GroupArgs& a, unsigned unit
     return it;
 }
 
-template <int D, int G>
+template <int D, int G, int QR>
 __global__ void __launch_bounds__(kThreads, 2)
     group_attention_kernel(const __grid_constant__ GroupArgs a, const __grid_constant__ CUtensorMap tmap_k,
                            const __grid_constant__ CUtensorMap tmap_v)
 {
-    using C = Cfg<D>;
+    using C = Cfg<D, QR>;
     constexpr int ST = C::ST, NH = C::NH;
-    extern __shared__ unsigned char smem_raw[];
-    unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    // dynamic shared memory starts on a 1024-byte boundary here (no static part; there is no room for a slack)
+    extern __shared__ __align__(1024) unsigned char smem[];
+    if ((smem_u32(smem) & 1023u) != 0) {
+        if (threadIdx.x == 0) atomicOr(a.status, PA_DEV_WAIT_TIMEOUT);
+        return;
+    }
     uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
     uint64_t* k_empty = k_full + ST;
     uint64_t* v_full = k_empty + ST;
@@ -171,52 +186,63 @@ __global__ void __launch_bounds__(kThreads, 2)
     pdl_launch_dependents();  // after it: a kernel that only needs the plan may start now
     const unsigned nunits = __ldcg(a.counts) * (unsigned)a.num_kv_heads;
 
-    if (warp == kProdWarp) {
+    if (warp == kKWarp || warp == kVWarp) {
+        const bool is_k = warp == kKWarp;
+        uint64_t* full = is_k ? k_full : v_full;
+        uint64_t* empty = is_k ? k_empty : v_empty;
+        const CUtensorMap* map = is_k ? &tmap_k : &tmap_v;
+        const uint32_t ring = smem_u32(smem) + (is_k ? C::OFF_K : C::OFF_V);
         const uint64_t pol = policy_evict_normal();
         bool ok = true;
-        int t = 0, nk = 0, nv = 0;  // tiles of finished units; K and V tiles issued
-        const int box = lane % kNBox, half = lane / kNBox;
-        for (unsigned u = blockIdx.x; u < nunits && ok; u += gridDim.x) {
-            const GroupItem it = load_item(a, u);
+        int t = 0;  // tiles issued
+        // physical block of box `lane` of tile j of a unit
+        auto lookup = [&](const GroupItem& it, int j) -> int {
+            const int tok = j * kTok + lane * kBox;
+            return lane < kNBox && tok < it.kvlen
+                       ? __ldg(a.block_tables + (size_t)it.table_row * a.max_blocks_per_seq + (it.kv0 + tok) / a.block_size)
+                       : 0;
+        };
+        unsigned u = blockIdx.x;
+        GroupItem it = load_item(a, u, nunits), nit = load_item(a, u + gridDim.x, nunits);
+        int next = lookup(it, 0);
+        for (; u < nunits && ok; u += gridDim.x) {
+            const GroupItem after = load_item(a, u + 2 * gridDim.x, nunits);
             const int kvh = (int)(u % (unsigned)a.num_kv_heads);
-            const int32_t* table = a.block_tables + (size_t)it.table_row * a.max_blocks_per_seq;
             const int n = (it.kvlen + kTok - 1) / kTok;
-            auto lookup = [&](int j) -> int {
-                const int tok = j * kTok + box * kBox;
-                return j < n && half < NH && tok < it.kvlen ? __ldg(table + (it.kv0 + tok) / a.block_size) : 0;
-            };
-            int next = lookup(0);
+            if (n == 0) next = lookup(nit, 0);
             for (int j = 0; j < n; ++j, ++t) {
                 int phys = next;
-                next = lookup(j + 1);
+                next = j + 1 < n ? lookup(it, j + 1) : lookup(nit, 0);
                 const int nbox = min(kNBox, (it.kvlen - j * kTok + kBox - 1) / kBox);
-                const bool mine = half < NH && box < nbox;
-                if (mine && (unsigned)phys >= (unsigned)a.num_blocks) {
+                if ((unsigned)phys >= (unsigned)a.num_blocks) {
                     atomicOr(a.status, PA_DEV_BAD_BLOCK);
                     phys = 0;
                 }
                 const int row = (phys * a.num_kv_heads + kvh) * a.block_size +
-                                (it.kv0 + j * kTok + box * kBox) % a.block_size;
-                const uint32_t tx = (uint32_t)(nbox * kBox * 128 * NH);
+                                (it.kv0 + j * kTok + lane * kBox) % a.block_size;
+                int rows[kNBox];
+#pragma unroll
+                for (int b = 0; b < kNBox; ++b) rows[b] = __shfl_sync(0xffffffffu, row, b);
                 const int st = t % ST;
-                const uint32_t off = st * C::TILE + half * C::KVHALF + box * kBox * 128;
+                // one thread issues the boxes (lanes of a warp that each issue one take turns, and take longer)
                 if (lane == 0) {
-                    if (t >= ST && !mbar_wait_bounded(&k_empty[st], ((t / ST) & 1) ^ 1, abort_flag)) ok = false;
-                    if (ok) mbar_arrive_expect_tx(&k_full[st], tx);
+                    if (t >= ST && !mbar_wait_bounded(&empty[st], ((t / ST) & 1) ^ 1, abort_flag)) ok = false;
+                    if (ok) {
+                        mbar_arrive_expect_tx(&full[st], (uint32_t)(nbox * kBox * 128 * NH));
+#pragma unroll
+                        for (int b = 0; b < kNBox; ++b)
+                            if (b < nbox)
+#pragma unroll
+                                for (int h = 0; h < NH; ++h)
+                                    tma_load_2d(ring + st * C::TILE + h * C::KVHALF + b * kBox * 128, map, h * 64, rows[b],
+                                                &full[st], pol);
+                    }
                 }
                 ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
                 if (!ok) break;
-                if (mine) tma_load_2d(smem_u32(smem + C::OFF_K + off), &tmap_k, half * 64, row, &k_full[st], pol);
-                ++nk;
-                if (lane == 0) {
-                    if (t >= ST && !mbar_wait_bounded(&v_empty[st], ((t / ST) & 1) ^ 1, abort_flag)) ok = false;
-                    if (ok) mbar_arrive_expect_tx(&v_full[st], tx);
-                }
-                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-                if (!ok) break;
-                if (mine) tma_load_2d(smem_u32(smem + C::OFF_V + off), &tmap_v, half * 64, row, &v_full[st], pol);
-                ++nv;
             }
+            it = nit;
+            nit = after;
         }
         if (lane == 0) {
             if (!ok) {
@@ -225,10 +251,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             // nothing may still be landing in shared memory when the CTA exits
             volatile int never = 0;
-            for (int i = max(0, nk - ST); i < nk; ++i)
-                if (!mbar_wait_bounded(&k_full[i % ST], (i / ST) & 1, &never)) atomicOr(a.status, PA_DEV_WAIT_TIMEOUT);
-            for (int i = max(0, nv - ST); i < nv; ++i)
-                if (!mbar_wait_bounded(&v_full[i % ST], (i / ST) & 1, &never)) atomicOr(a.status, PA_DEV_WAIT_TIMEOUT);
+            for (int i = max(0, t - ST); i < t; ++i)
+                if (!mbar_wait_bounded(&full[i % ST], (i / ST) & 1, &never)) atomicOr(a.status, PA_DEV_WAIT_TIMEOUT);
         }
     } else if (warp == kMmaWarp) {
         if (lane == 0) {
@@ -259,19 +283,15 @@ __global__ void __launch_bounds__(kThreads, 2)
             };
             bool ok = true;
             int t = 0;       // tiles whose P V was issued
-            int done = 0;    // units finished
+            int done = 0;    // units with tokens finished
             unsigned u = blockIdx.x;
-            auto tiles_of = [&](unsigned unit) { return (load_item(a, unit).kvlen + kTok - 1) / kTok; };
-            int n = 0;
-            for (; u < nunits; u += gridDim.x)
-                if ((n = tiles_of(u)) > 0) break;
-            if (u < nunits) ok = issue_qk(0, true);
-            while (ok && u < nunits) {
-                // the next unit with tokens
-                unsigned un = u + gridDim.x;
-                int nn = 0;
-                for (; un < nunits; un += gridDim.x)
-                    if ((nn = tiles_of(un)) > 0) break;
+            auto tiles_of = [&](unsigned unit) {
+                return unit < nunits ? (__ldcg(&a.items[unit / (unsigned)a.num_kv_heads].kvlen) + kTok - 1) / kTok : 0;
+            };
+            int n = tiles_of(u), nn = tiles_of(u + gridDim.x);
+            if (n > 0) ok = issue_qk(0, true);
+            for (; ok && u < nunits; u += gridDim.x) {
+                const int after = tiles_of(u + 2 * gridDim.x);
                 for (int j = 0; j < n && ok; ++j, ++t) {
                     if (j + 1 < n && !(ok = issue_qk(t + 1, false))) break;
                     if (!mbar_wait_bounded(&p_full[t & 1], (t >> 1) & 1, abort_flag) ||
@@ -289,10 +309,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                     umma_commit(o_done);
                     umma_commit(&v_empty[t % ST]);
                 }
-                ++done;
-                u = un;
+                done += n > 0 ? 1 : 0;
                 n = nn;
-                if (ok && u < nunits) ok = issue_qk(t, true);
+                nn = after;
+                if (ok && n > 0) ok = issue_qk(t, true);
             }
             if (!ok) {
                 atomicOr(a.status, PA_DEV_WAIT_TIMEOUT);
@@ -310,13 +330,14 @@ __global__ void __launch_bounds__(kThreads, 2)
         const float sl = neg ? -a.scale_log2 : a.scale_log2;
         const uint64_t slp = pack2f(sl, sl);
         bool ok = true;
-        int t = 0, done = 0;
+        int t = 0;
         auto query_row = [&](const GroupItem& it) {
-            const int i = it.row0 + min(member, it.members - 1);
-            return a.rows ? __ldg(a.rows + i) : i;
+            const int i = it.row0 + max(0, min(member, it.members - 1));
+            return a.rows && it.members > 0 ? __ldg(a.rows + i) : i;
         };
         // this row of the unit's Q into shared memory, 16 bytes at a time
-        auto fetch_q = [&](int row, int kvh) {
+        auto fetch_q = [&](const GroupItem& it, int row, int kvh) {
+            if (member >= it.members) return;
             const char* src = static_cast<const char*>(a.q) +
                               (((size_t)row * a.num_heads) + (size_t)kvh * G + head) * (D * 2);
             const uint32_t dst = smem_u32(smem) + r * 128;
@@ -330,36 +351,38 @@ __global__ void __launch_bounds__(kThreads, 2)
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full);
         };
-        // the first unit from u on that has tokens; rows of the others get zeros
-        auto settle = [&](unsigned u, GroupItem& it) -> unsigned {
-            for (; u < nunits; u += gridDim.x) {
-                it = load_item(a, u);
-                if (it.kvlen > 0) break;
-                if (member < it.members) {
-                    const size_t o = (size_t)query_row(it) * a.num_heads + (u % (unsigned)a.num_kv_heads) * G + head;
-                    uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + o * D);
-                    for (int c = 0; c < D / 8; ++c) out[c] = make_uint4(0, 0, 0, 0);
-                    if (a.lse) a.lse[o] = -INFINITY;
-                }
-            }
-            return u;
-        };
-        GroupItem it;
-        unsigned u = settle(blockIdx.x, it);
-        int row = 0;
-        if (u < nunits) {
-            row = query_row(it);
-            fetch_q(row, (int)(u % (unsigned)a.num_kv_heads));
+        unsigned u = blockIdx.x;
+        GroupItem it = load_item(a, u, nunits), nit = load_item(a, u + gridDim.x, nunits);
+        int row = query_row(it);
+        if (it.kvlen > 0) {
+            fetch_q(it, row, (int)(u % (unsigned)a.num_kv_heads));
             q_ready();
         }
-        while (u < nunits) {
+        for (; u < nunits; u += gridDim.x) {
+            const GroupItem after = load_item(a, u + 2 * gridDim.x, nunits);
+            const int nrow = query_row(nit);
             const int kvh = (int)(u % (unsigned)a.num_kv_heads);
+            const int nkvh = (int)((u + gridDim.x) % (unsigned)a.num_kv_heads);
             const int n = (it.kvlen + kTok - 1) / kTok;
             const bool valid = member < it.members;
             const bool active = (warp * 32) / G < it.members;  // the warp has a valid row
-            GroupItem nit;
-            const unsigned un = settle(u + gridDim.x, nit);
-            const int nrow = un < nunits ? query_row(nit) : 0;
+            const size_t o_row = (size_t)row * a.num_heads + (size_t)kvh * G + head;
+            if (n == 0) {
+                // no tokens: the rows are zero
+                if (valid) {
+                    uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + o_row * D);
+                    for (int c = 0; c < D / 8; ++c) out[c] = make_uint4(0, 0, 0, 0);
+                    if (a.lse) a.lse[o_row] = -INFINITY;
+                }
+                if (nit.kvlen > 0) {
+                    fetch_q(nit, nrow, nkvh);
+                    q_ready();
+                }
+                it = nit;
+                nit = after;
+                row = nrow;
+                continue;
+            }
             float m_used = -INFINITY, l = 0.f;
             for (int j = 0; j < n; ++j, ++t) {
                 if (!mbar_wait_warp(&s_full[t & 1], (t >> 1) & 1, abort_flag)) {
@@ -368,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
                 tc_fence_after_sync();
                 // every Q K^T of the unit has finished: the next unit's Q may take its place
-                if (j == n - 1 && un < nunits) fetch_q(nrow, (int)(un % (unsigned)a.num_kv_heads));
+                if (j == n - 1 && nit.kvlen > 0) fetch_q(nit, nrow, nkvh);
                 const int left = it.kvlen - j * kTok;  // tokens from this tile on
                 if (active) {
                     uint32_t sr[2][32];
@@ -398,7 +421,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                     const float mraw = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
                                              fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
                     const float m_new = fmaxf(m_used, mraw == -INFINITY ? -INFINITY : mraw * sl);
-                    const bool rescale = m_used != -INFINITY && m_new > m_used + kLazy;
+                    // (rows that are not valid hold whatever was in shared memory: they may not cause the others work)
+                    const bool rescale = valid && m_used != -INFINITY && m_new > m_used + kLazy;
                     const float alpha = rescale ? ex2(m_used - m_new) : 1.f;
                     if (rescale || m_used == -INFINITY) m_used = m_new;
                     const float mref = m_used == -INFINITY ? 0.f : m_used;
@@ -452,19 +476,25 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                     fence_async_smem();
                 }
+                // S of this tile was issued before P V of the tile before it, which may still be waiting for a
+                // slower warp.  The wait for this tile's P V below is on a one-bit parity, so P V of the tile
+                // before has to be known finished first, and while this tile's cannot be.
+                if (j > 0 && j == n - 1 && !mbar_wait_warp(o_done, (t - 1) & 1, abort_flag)) {
+                    ok = false;
+                    break;
+                }
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[t & 1]);
             }
             if (!ok) break;
-            if (un < nunits) q_ready();
+            if (nit.kvlen > 0) q_ready();
             if (!mbar_wait_warp(o_done, (t - 1) & 1, abort_flag)) {
                 ok = false;
                 break;
             }
             tc_fence_after_sync();
             if (active) {
-                const size_t o_row = (size_t)row * a.num_heads + (size_t)kvh * G + head;
                 const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
@@ -501,9 +531,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(o_free);
-            ++done;
-            u = un;
             it = nit;
+            nit = after;
             row = nrow;
         }
         if (!ok) {
@@ -593,12 +622,11 @@ __global__ void __launch_bounds__(128) group_merge_kernel(const GroupArgs a)
 // (tokens x tiles x kv heads) over twice the resident CTAs, at least 256 tokens.
 constexpr int kPlanThreads = 1024;
 
-__global__ void __launch_bounds__(kPlanThreads) cross_plan_kernel(const CrossArgs a, int group, int ctas)
+__global__ void __launch_bounds__(kPlanThreads) cross_plan_kernel(const CrossArgs a, int T, int ctas)
 {
     __shared__ unsigned long long s_work;
     __shared__ unsigned s_items, s_merges;
     pdl_launch_dependents();
-    const int T = kRows / group;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int cap = min(a.max_context_len, (int)min((long long)a.g.max_blocks_per_seq * a.g.block_size, 0x7fffffffll));
     if (threadIdx.x == 0) {
@@ -674,31 +702,37 @@ int sm_count()
     return sms;
 }
 
-template <int D, int G>
-cudaError_t launch_group_dg(const GroupArgs& a, cudaStream_t stream)
+template <int D, int G, int QR>
+cudaError_t launch_group_dgq(const GroupArgs& a, int ctas, cudaStream_t stream)
 {
-    using C = Cfg<D>;
+    using C = Cfg<D, QR>;
     CUtensorMap tk, tv;
     const uint64_t rows = (uint64_t)a.num_blocks * a.num_kv_heads * a.block_size;
     cudaError_t e = encode_pool_map(&tk, a.k_cache, rows, D, kBox);
     if (e != cudaSuccess) return e;
     if ((e = encode_pool_map(&tv, a.v_cache, rows, D, kBox)) != cudaSuccess) return e;
-    if ((e = cudaFuncSetAttribute(group_attention_kernel<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if ((e = cudaFuncSetAttribute(group_attention_kernel<D, G, QR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   C::SMEM)) != cudaSuccess)
         return e;
     const int64_t units = (int64_t)a.max_entries * a.num_kv_heads;
-    const unsigned grid = (unsigned)std::min<int64_t>(units, group_resident_ctas(sm_count()));
-    return launch_pdl(group_attention_kernel<D, G>, dim3(grid), dim3(kThreads), (size_t)C::SMEM, stream, a, tk, tv);
+    const unsigned grid = (unsigned)std::min<int64_t>(units, ctas);
+    return launch_pdl(group_attention_kernel<D, G, QR>, dim3(grid), dim3(kThreads), (size_t)C::SMEM, stream, a, tk, tv);
+}
+
+template <int D, int G>
+cudaError_t launch_group_dg(const GroupArgs& a, int tile_rows, int ctas, cudaStream_t stream)
+{
+    return tile_rows == 64 ? launch_group_dgq<D, G, 64>(a, ctas, stream) : launch_group_dgq<D, G, 128>(a, ctas, stream);
 }
 
 template <int D>
-cudaError_t launch_group_d(const GroupArgs& a, int group, cudaStream_t stream)
+cudaError_t launch_group_d(const GroupArgs& a, int group, int tile_rows, int ctas, cudaStream_t stream)
 {
     switch (group) {
-        case 1: return launch_group_dg<D, 1>(a, stream);
-        case 2: return launch_group_dg<D, 2>(a, stream);
-        case 4: return launch_group_dg<D, 4>(a, stream);
-        case 8: return launch_group_dg<D, 8>(a, stream);
+        case 1: return launch_group_dg<D, 1>(a, tile_rows, ctas, stream);
+        case 2: return launch_group_dg<D, 2>(a, tile_rows, ctas, stream);
+        case 4: return launch_group_dg<D, 4>(a, tile_rows, ctas, stream);
+        case 8: return launch_group_dg<D, 8>(a, tile_rows, ctas, stream);
         default: return cudaErrorInvalidValue;
     }
 }
@@ -707,9 +741,10 @@ cudaError_t launch_group_d(const GroupArgs& a, int group, cudaStream_t stream)
 
 int group_resident_ctas(int sms) { return 2 * sms; }
 
-cudaError_t launch_group(const GroupArgs& a, int head_dim, int group, cudaStream_t stream)
+cudaError_t launch_group(const GroupArgs& a, int head_dim, int group, int tile_rows, int ctas, cudaStream_t stream)
 {
-    return head_dim == 64 ? launch_group_d<64>(a, group, stream) : launch_group_d<128>(a, group, stream);
+    return head_dim == 64 ? launch_group_d<64>(a, group, tile_rows, ctas, stream)
+                          : launch_group_d<128>(a, group, tile_rows, ctas, stream);
 }
 
 cudaError_t launch_group_merge(const GroupArgs& a, int head_dim, cudaStream_t stream)
@@ -722,10 +757,12 @@ cudaError_t launch_group_merge(const GroupArgs& a, int head_dim, cudaStream_t st
 
 cudaError_t launch_cross(const CrossArgs& a, int head_dim, int group, cudaStream_t stream)
 {
-    cross_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, group, group_resident_ctas(sm_count()));
+    const int ctas = group_resident_ctas(sm_count());
+    const int tile_rows = (int64_t)a.max_query_len * group <= 64 ? 64 : 128;
+    cross_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, tile_rows / group, ctas);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    if ((e = launch_group(a.g, head_dim, group, stream)) != cudaSuccess) return e;
+    if ((e = launch_group(a.g, head_dim, group, tile_rows, ctas, stream)) != cudaSuccess) return e;
     return a.max_chunks > 1 ? launch_group_merge(a.g, head_dim, stream) : cudaSuccess;
 }
 

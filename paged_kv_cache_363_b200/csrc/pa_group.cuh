@@ -13,7 +13,7 @@ namespace pa {
 struct GroupItem {
     int table_row;   // row of block_tables
     int row0;        // first member: an index into rows[] (or the query row itself when rows is null)
-    int members;     // at most 128 / G
+    int members;     // at most the launch's rows of a tile (64 or 128) / G
     int chunk;       // partial state this entry writes, or -1: it writes the output
     int kv0, kvlen;  // tokens [kv0, kv0 + kvlen); kv0 a multiple of 64
     int pad[2];
@@ -76,9 +76,9 @@ inline int group_max_chunks(int64_t max_len, int64_t rows, int group, int num_kv
 // CTAs of the kernel resident on the device at once.
 int group_resident_ctas(int sms);
 
-// The kernel over the entries a plan kernel (just launched on the stream) wrote; then, when
-// `merge` is set, the merge of the rows it listed.
-cudaError_t launch_group(const GroupArgs& a, int head_dim, int group, cudaStream_t stream);
+// The kernel over the entries a plan kernel (just launched on the stream) wrote, tiles of
+// tile_rows rows, on at most `ctas` CTAs; and the merge of the rows the plan listed.
+cudaError_t launch_group(const GroupArgs& a, int head_dim, int group, int tile_rows, int ctas, cudaStream_t stream);
 cudaError_t launch_group_merge(const GroupArgs& a, int head_dim, cudaStream_t stream);
 
 // pa_cross_attention: plan, kernel, merge.

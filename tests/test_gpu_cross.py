@@ -164,3 +164,22 @@ def test_cross_flags_and_skips_bad_sequences(pa):
     torch.cuda.synchronize()
     assert pa.pa_device_status() == pa.PA_DEV_BAD_BLOCK
     assert torch.equal(out[:5], good[:5]) and torch.equal(out[11:], good[11:])
+
+
+@pytest.mark.parametrize("Hkv,G,D,lens,rows", [
+    (2, 4, 128, [200] * 100, [100] * 100), (1, 4, 128, [8192] * 4, [100] * 4), (4, 1, 64, [900, 257, 1, 640], [700, 129, 300, 513]),
+    (8, 4, 128, [1, 900] * 20, [100] * 40)])
+def test_cross_same_bits_in_every_run(pa, Hkv, G, D, lens, rows):
+    """All four softmax warps busy, two CTAs per SM, warps that run ahead of each other: nothing may depend on it."""
+    p = Paged(lens, Hkv, 16, D, torch.bfloat16, seed=21)
+    q = p.q(sum(rows), Hkv * G).cuda()
+    k, v, tables, ctx = p.cuda()
+    start = torch.from_numpy(np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)).cuda()
+    outs = []
+    for _ in range(25):
+        out = torch.empty_like(q)
+        pa.pa_cross_attention(out, q, k, v, tables, ctx, start, max(rows), max(lens), D ** -0.5)
+        outs.append(out)
+    torch.cuda.synchronize()
+    assert pa.pa_device_status() == 0
+    assert all(torch.equal(o, outs[0]) for o in outs)
