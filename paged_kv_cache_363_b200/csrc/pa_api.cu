@@ -774,11 +774,6 @@ pa_status pa_decode_shared(void* out, const void* q, const void* k_cache, const 
         set_error("pa_decode_shared: bad size or scale (a row is in one group at most)");
         return PA_ERR_INVALID;
     }
-    if ((max_context_len + (int64_t)kMaxPartitionTokens - 1) / kMaxPartitionTokens > kMaxPartitions) {
-        set_error("pa_decode_shared: max_context_len exceeds " + std::to_string(kMaxPartitions) + " partitions of " +
-                  std::to_string(kMaxPartitionTokens) + " tokens");
-        return PA_ERR_UNSUPPORTED;
-    }
     if (num_seqs == 0) return PA_OK;
     if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens ||
         (num_groups > 0 && (!group_start || !shared_lens)) || (num_group_rows > 0 && !group_rows)) {
@@ -827,45 +822,27 @@ pa_status pa_decode_shared(void* out, const void* q, const void* k_cache, const 
     a.g.block_size = block_size;
     a.g.num_partitions = w.chunks + w.parts;
     a.g.lead_partitions = w.chunks;
-    a.g.max_entries = num_groups > 0 ? (int)w.entries : 0;
+    a.g.max_entries = (int)w.entries;
     a.g.scale_log2 = scale * 1.4426950408889634f;
-    a.d.out = out;
-    a.d.q = q;
-    a.d.k_cache = k_cache;
-    a.d.v_cache = v_cache;
-    a.d.block_tables = block_tables;
-    a.d.context_lens = context_lens;
-    a.d.plan = reinterpret_cast<unsigned*>(ws + w.plan);
-    a.d.plan_list = reinterpret_cast<uint2*>(ws + w.list);
-    a.d.ws_acc = reinterpret_cast<float*>(ws + w.acc);
-    a.d.ws_ml = reinterpret_cast<float*>(ws + w.ml);
-    a.d.status = status;
-    a.d.num_seqs = num_seqs;
-    a.d.num_heads = num_heads;
-    a.d.num_kv_heads = num_kv_heads;
-    a.d.max_blocks_per_seq = max_blocks_per_seq;
-    a.d.num_blocks = num_blocks;
-    a.d.max_context_len = max_context_len;
-    a.d.partition_blocks = shared_partition(max_context_len) / block_size;
-    a.d.adaptive = 1;
-    a.d.num_partitions = w.chunks + w.parts;
-    a.d.lead_partitions = w.chunks;
-    a.d.scale_log2 = a.g.scale_log2;
+    a.context_lens = context_lens;
     a.group_rows = group_rows;
     a.group_start = group_start;
     a.shared_lens = shared_lens;
-    a.row_info = ws + w.row_info;
+    a.own = reinterpret_cast<OwnItem*>(ws + w.own);
+    a.arrived = reinterpret_cast<unsigned*>(ws + w.arrived);
     a.listed = reinterpret_cast<int*>(ws + w.listed);
     a.ctx = reinterpret_cast<int*>(ws + w.ctx);
     a.lead_blocks = reinterpret_cast<int*>(ws + w.lead_blocks);
     a.lead_states = reinterpret_cast<int*>(ws + w.lead_states);
     a.group_ok = reinterpret_cast<int*>(ws + w.group_ok);
+    a.num_seqs = num_seqs;
     a.num_groups = num_groups;
     a.num_group_rows = num_group_rows;
+    a.max_context_len = max_context_len;
     a.max_shared_len = max_shared_len;
     a.max_chunks = w.chunks;
-    const cudaError_t e =
-        launch_shared(a, head_dim, block_size, num_heads / num_kv_heads, static_cast<cudaStream_t>(stream));
+    a.max_parts = w.parts;
+    const cudaError_t e = launch_shared(a, head_dim, num_heads / num_kv_heads, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail("pa_decode_shared launch", e);
     return PA_OK;
 }

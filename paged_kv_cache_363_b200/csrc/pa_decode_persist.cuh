@@ -1,7 +1,6 @@
-// The persistent decode kernel and its launch size, shared by the decode calls: pa_decode
-// (pa_decode.cu), pa_decode_scores (pa_decode_scores.cu) and pa_decode_shared
-// (pa_shared.cu).  MODE picks what a unit does beside its attention; the plain form's
-// code has none of the others' (every difference is resolved at compile time).
+// The persistent decode kernel and its launch, shared by pa_decode (pa_decode.cu) and
+// pa_decode_scores (pa_decode_scores.cu).  MODE picks what a unit does beside its attention;
+// the plain form's code has nothing of the other's (it is resolved at compile time).
 #pragma once
 
 #include <cuda.h>
@@ -24,7 +23,6 @@ namespace {
 
 constexpr int kModePlain = 0;   // pa_decode
 constexpr int kModeScores = 1;  // also writes every token's logits and every partition's (max, sum)
-constexpr int kModeOwn = 2;     // a sequence's own tokens, behind the blocks it shares (uint4 list entries)
 
 constexpr int kEndUnit = 1;    // no more work for this CTA
 constexpr int kSplitUnit = 2;  // the sequence spans several partitions
@@ -151,9 +149,7 @@ __global__ void __launch_bounds__(Persist<Cons, BS>::THREADS, 2)
     // only its unit producer waits for the plan, before its second unit.  Every other
     // CTA waits here; the plan kernel's list and counters are visible after the wait.
     const bool early = (int)blockIdx.x < a.first_wave;
-    // (kModeOwn: the kernel before this one starts it only after it has waited for the plan,
-    // unless that kernel is the plan.)
-    if (MODE == kModeOwn ? a.wait_first != 0 : !early) pdl_wait_primary();
+    if (!early) pdl_wait_primary();
 
     auto slot = [&](int k) { return smem + P::OFF_SLOT + (k % UR) * P::SLOT_BYTES; };
     auto slot_table = [&](int k) { return reinterpret_cast<int*>(slot(k) + P::QBYTES); };
@@ -166,23 +162,14 @@ __global__ void __launch_bounds__(Persist<Cons, BS>::THREADS, 2)
         // most one CTA per unit the list can hold).  A first-wave CTA knows its first
         // unit without the list: partition 0 of sequence b / Hkv (the plan puts that
         // pair at list position b / Hkv).
-        // In kModeOwn an entry has two words more: the blocks before the sequence's own
-        // ones, and the partial states of its shared tokens (no first wave there).
         unsigned nunits = 0;
         uint2 e_first;
-        uint2 x_first = make_uint2(0u, 0u);
         auto plan_ready = [&]() { nunits = __ldcg(a.plan + 1) * (unsigned)a.num_kv_heads; };
         if (early) {
             const int s0 = (int)(blockIdx.x / (unsigned)a.num_kv_heads);
             e_first = make_uint2((unsigned)s0 << 11, (unsigned)clamped_context(a, s0, B, false));
         } else {
-            if constexpr (MODE == kModeOwn) {
-                const uint4 e4 = __ldcg(reinterpret_cast<const uint4*>(a.plan_list) + blockIdx.x / (unsigned)a.num_kv_heads);
-                e_first = make_uint2(e4.x, e4.y);
-                x_first = make_uint2(e4.z, e4.w);
-            } else {
-                e_first = __ldcg(a.plan_list + blockIdx.x / (unsigned)a.num_kv_heads);
-            }
+            e_first = __ldcg(a.plan_list + blockIdx.x / (unsigned)a.num_kv_heads);
             plan_ready();
         }
         // This CTA takes no more units.  The last CTA to stop (at the end marker or on
@@ -229,26 +216,15 @@ __global__ void __launch_bounds__(Persist<Cons, BS>::THREADS, 2)
                 ended = true;
                 break;
             }
-            uint2 e, x = x_first;
-            if constexpr (MODE == kModeOwn) {
-                e = e_first;
-                if (k > 0) {
-                    const uint4 e4 = __ldcg(reinterpret_cast<const uint4*>(a.plan_list) + u / (unsigned)a.num_kv_heads);
-                    e = make_uint2(e4.x, e4.y);
-                    x = make_uint2(e4.z, e4.w);
-                }
-            } else {
-                e = k == 0 ? e_first : a.plan_list[u / (unsigned)a.num_kv_heads];
-            }
+            const uint2 e = k == 0 ? e_first : a.plan_list[u / (unsigned)a.num_kv_heads];
             const int kvh = (int)(u % (unsigned)a.num_kv_heads);
             const int s = (int)(e.x >> 11);
             const int part = (int)(e.x & 2047u);
             const int L = (int)e.y;
-            const int lead = MODE == kModeOwn ? (int)x.x : 0;  // blocks before the unit's sequence
-            const int nblk_seq = (L + B - 1) / B - lead;
+            const int nblk_seq = (L + B - 1) / B;
             const int pb = (k == 0 && early) ? a.partition_blocks : (int)a.plan[2];  // equal when early
-            const int b0 = lead + part * pb;
-            const int nb = max(0, min(pb, nblk_seq - part * pb));
+            const int b0 = part * pb;
+            const int nb = max(0, min(pb, nblk_seq - b0));
             int* tab = slot_table(k);
             // A first-wave unit reads its table slice (partition 0: the row's first pb
             // entries, all inside the row) in the same trip to memory as its context
@@ -264,7 +240,7 @@ __global__ void __launch_bounds__(Persist<Cons, BS>::THREADS, 2)
                 info->b0 = b0;
                 info->first = first;
                 info->L = L;
-                info->flags = nblk_seq > pb || (MODE == kModeOwn && x.y > 0) ? kSplitUnit : 0;
+                info->flags = nblk_seq > pb ? kSplitUnit : 0;
                 info->np = (nblk_seq + pb - 1) / pb;
             }
             __syncwarp();
@@ -276,9 +252,6 @@ __global__ void __launch_bounds__(Persist<Cons, BS>::THREADS, 2)
             }
             first += nb * SPB;
         }
-        // The shared tokens' kernel may still run beside this one, which never reads its
-        // results: wait for it here, so that whatever waits for this grid has both.
-        if constexpr (MODE == kModeOwn) pdl_wait_primary();
         // No q copy may still be landing in shared memory at exit: wait for the fills of
         // the last units.  After an end marker, slot k % UR has moved on past unit k - UR
         // (a parity wait on that older phase would alias), so only units k-UR+1 .. k-1.
@@ -387,8 +360,7 @@ __global__ void __launch_bounds__(Persist<Cons, BS>::THREADS, 2)
                 }
                 const bool split = (info->flags & kSplitUnit) != 0;
                 finish_unit_warp<T, D, G, NCW, MODE == kModeScores>(
-                    a, mg_m, mg_l, mg_acc, info->s, info->kvh, info->part + (MODE == kModeOwn ? a.lead_partitions : 0),
-                    split, first % NCW, lane);
+                    a, mg_m, mg_l, mg_acc, info->s, info->kvh, info->part, split, first % NCW, lane);
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(mg_free);

@@ -60,8 +60,6 @@ struct DecodeArgs {
     float* logits;             // pa_decode_scores: [S][Hkv][max_context_len][G] base-2 logits
     float* scores;             // pa_decode_scores: [S][Hkv][score_stride]
     int score_stride;
-    int lead_partitions;       // pa_decode_shared: partial states kept for the shared tokens, before a row's own
-    int wait_first;            // pa_decode_shared: the kernel before this one is the plan itself
 };
 
 constexpr int kDecodePlan = 1;  // the plan kernel: work list into the workspace

@@ -6,22 +6,22 @@
 //   out = sum 2^(m_p - M) O_p / sum 2^(m_p - M) l_p,  M = max m_p.
 // The shared tokens of a kv head are one dense product of all the group's rows x G query
 // heads with the same K and V: the tensor-core kernel of pa_group.cu reads each shared byte
-// once per 128 rows, where pa_decode reads it once per sequence (from L2 when it is lucky).
-// A row's own tokens are read by the kernel that also joins the states, unless they are many;
-// those go through pa_decode's persistent kernel, from the block behind the shared ones.
+// once per tile of rows, where pa_decode reads it once per sequence (from L2 when it is lucky).
 //
-// Four kernels: a plan, the shared tokens, the long rows' own tokens, the finish.  The last two
-// need the plan alone to begin, so the shared tokens' kernel lets them start once it has itself
-// seen the plan finish, and the CTAs of all share the device until the work is gone.
+// Three kernels: a plan, the shared tokens, and the own tokens with the join.  The last needs
+// the plan alone to begin, so the shared tokens' kernel lets it start once it has itself seen
+// the plan finish, and its CTAs fill the places that the other's leave.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
-#include "pa_decode_persist.cuh"
+#include "pa_decode_mma.cuh"
 #include "pa_group.cuh"
 #include "pa_internal.h"
 #include "pa_launch.cuh"
+#include "pa_ptx.cuh"
 #include "pa_shared.h"
 
 namespace pa {
@@ -29,24 +29,13 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 
-// 16 bytes of the K/V stream, read once
-__device__ __forceinline__ uint4 ldg_stream(const uint4* p)
+// Entry i, or one without tokens past the end.
+__device__ __forceinline__ OwnItem load_own(const OwnItem* items, unsigned i, unsigned n)
 {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
+    if (i >= n) return OwnItem{0, 0, 0, 0, 0, 1, {0, 0}};
+    const int4 x = __ldcg(reinterpret_cast<const int4*>(items + i)), y = __ldcg(reinterpret_cast<const int4*>(items + i) + 1);
+    return OwnItem{x.x, x.y, x.z, x.w, y.x, y.y, {0, 0}};
 }
-
-// What the plan says about a row.
-struct RowInfo {
-    int lead_blocks;   // shared blocks before its own tokens
-    int lead_states;   // partial states of its shared tokens
-    int own_parts;     // partial states of its own tokens (kDirect: none, the finish attends to them itself)
-    int L;             // context length (clamped)
-};
-constexpr int kDirect = -1;
 
 // The plan, in one CTA.
 //  1. Groups are checked (starts in order, rows in range and listed once, whole blocks, no more
@@ -54,37 +43,41 @@ constexpr int kDirect = -1;
 //     shared: its rows attend to all their tokens on their own, which is the same result.
 //  2. Entries of the shared tokens: (tile of rows, chunk), a chunk's tiles next to each other.
 //     The chunk length is the work over twice the resident CTAs, at least 256 tokens.
-//  3. The long rows' own tokens as units for the decode kernel, longest first, as pa_decode's
-//     plan lists them, each entry with the blocks before it and the number of shared states
-//     (which makes it write its own state).
+//  3. Entries of the own tokens: a row, or one of its parts, the longer half of the entries
+//     first.  A part is half a warp's share of all own tokens, at least 256 (joining a row's
+//     parts costs some 4 us) and as many as keep the row within its partial states.
 // A batch of up to 1024 rows keeps its per-row values in shared memory: the plan is on the
 // critical path, and most of it was trips to L2.
-__global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const SharedArgs a, int T, int group_ctas)
+__global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const SharedArgs a, int T, int group_ctas, int own_warps)
 {
-    __shared__ int bucket[kMaxPartitionTokens / 16 + 1];
     __shared__ int s_listed[kPlanThreads], s_ctx[kPlanThreads], s_lead[kPlanThreads], s_states[kPlanThreads];
-    __shared__ unsigned long long s_work, s_tok;
-    __shared__ unsigned s_items;
-    __shared__ int s_bad, s_max, s_pb;
+    __shared__ unsigned long long s_work, s_own;
+    __shared__ unsigned s_items, s_big, s_front, s_back;
+    __shared__ int s_bad;
     pdl_launch_dependents();
-    const DecodeArgs& d = a.d;
-    const int B = a.g.block_size;
+    const int B = a.g.block_size, S = a.num_seqs;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const bool small = d.num_seqs <= kPlanThreads;
+    const bool small = S <= kPlanThreads;
     volatile int* listed = small ? s_listed : a.listed;
     volatile int* ctx = small ? s_ctx : a.ctx;
     volatile int* lead_blocks = small ? s_lead : a.lead_blocks;
     volatile int* lead_states = small ? s_states : a.lead_states;
     if (tid == 0) {
-        s_work = s_tok = 0;
-        s_items = 0;
-        s_bad = s_max = 0;
+        s_work = s_own = 0;
+        s_items = s_big = s_front = s_back = 0;
+        s_bad = 0;
     }
-    for (int s = tid; s < d.num_seqs; s += kPlanThreads) {
+    const int cap = min(a.max_context_len, (int)min((long long)a.g.max_blocks_per_seq * B, 0x7fffffffll));
+    for (int s = tid; s < S; s += kPlanThreads) {
         listed[s] = 0;
         lead_blocks[s] = 0;
         lead_states[s] = 0;
-        ctx[s] = clamped_context(d, s, B, true);
+        int L = __ldg(a.context_lens + s);
+        if (L < 0 || L > cap) {
+            atomicOr(a.g.status, PA_DEV_BAD_CONTEXT);
+            L = L < 0 ? 0 : cap;
+        }
+        ctx[s] = L;
     }
     __syncthreads();
     for (int g = tid; g < a.num_groups; g += kPlanThreads) {
@@ -93,29 +86,29 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
     }
     for (int i = tid; i < a.num_group_rows; i += kPlanThreads) {
         const int s = __ldg(a.group_rows + i);
-        if ((unsigned)s < (unsigned)d.num_seqs) atomicAdd(const_cast<int*>(listed) + s, 1);
+        if ((unsigned)s < (unsigned)S) atomicAdd(const_cast<int*>(listed) + s, 1);
     }
     __syncthreads();
-    if (tid == 0 && s_bad) atomicOr(d.status, PA_DEV_BAD_CONTEXT);
+    if (tid == 0 && s_bad) atomicOr(a.g.status, PA_DEV_BAD_CONTEXT);
     const int ngroups = s_bad ? 0 : a.num_groups;
     for (int g = warp; g < ngroups; g += kPlanThreads / 32) {
         const int r0 = __ldg(a.group_start + g), r1 = __ldg(a.group_start + g + 1), n = __ldg(a.shared_lens + g);
         bool ok = n >= 0 && n <= a.max_shared_len && n % B == 0;
         for (int i = r0 + lane; i < r1; i += 32) {
             const int s = __ldg(a.group_rows + i);
-            ok = ok && (unsigned)s < (unsigned)d.num_seqs;
+            ok = ok && (unsigned)s < (unsigned)S;
             ok = ok && listed[s] == 1 && n <= ctx[s];
         }
         ok = __all_sync(0xffffffffu, ok) != 0;
         if (lane == 0) {
             a.group_ok[g] = ok && n > 0 && r1 > r0;
-            if (!ok) atomicOr(d.status, PA_DEV_BAD_CONTEXT);
+            if (!ok) atomicOr(a.g.status, PA_DEV_BAD_CONTEXT);
             else if (n > 0) atomicAdd(&s_work, (unsigned long long)((r1 - r0 + T - 1) / T) * n);
         }
     }
     __syncthreads();
     if (s_work > 0) {
-        const unsigned long long share = s_work * d.num_kv_heads / (2ull * group_ctas);
+        const unsigned long long share = s_work * a.g.num_kv_heads / (2ull * group_ctas);
         const int least = (a.max_shared_len + a.max_chunks - 1) / a.max_chunks;
         const int chunk = (max(max((int)min(share, 1ull << 30), least), 256) + 63) / 64 * 64;
         GroupItem* items = const_cast<GroupItem*>(a.g.items);
@@ -149,377 +142,482 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
         }
         __syncthreads();
     }
-    // ---- the own tokens of long rows
-    auto long_len = [&](int s) {
-        const int own = ctx[s] - lead_blocks[s] * B;
-        return own > kDirectTokens ? own : 0;
-    };
     unsigned long long tok = 0;
-    int lmax = 0;
-    for (int s = tid; s < d.num_seqs; s += kPlanThreads) {
-        const int L = long_len(s);
-        tok += (unsigned long long)L;
-        lmax = max(lmax, L);
+    for (int s = tid; s < S; s += kPlanThreads) tok += (unsigned long long)(ctx[s] - lead_blocks[s] * B);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) tok += __shfl_xor_sync(0xffffffffu, tok, o);
+    if (lane == 0 && tok) atomicAdd(&s_own, tok);
+    __syncthreads();
+    const int share = (int)min(s_own * a.g.num_kv_heads / (2ull * own_warps), 1ull << 30);
+    // tokens of a row's parts, all the same but the last
+    auto part_of = [&](int own) {
+        const int least = (own + a.max_parts - 1) / a.max_parts;
+        const int p = (max(max(share, least), 256) + 15) / 16 * 16;
+        const int n = (own + p - 1) / p;
+        return n <= 1 ? max(own, 1) : ((own + n - 1) / n + 15) / 16 * 16;
+    };
+    const int big = max(32, share / 2);  // an entry of the first half
+    unsigned nbig = 0;
+    for (int s = tid; s < S; s += kPlanThreads) {
+        const int own = ctx[s] - lead_blocks[s] * B, per = part_of(own);
+        nbig += per > big ? (unsigned)((own + per - 1) / per) : 0u;
     }
-    if (tok > 0) {
-        atomicAdd(&s_tok, tok);
-        atomicMax(&s_max, lmax);
+    if (nbig) atomicAdd(&s_big, nbig);
+    __syncthreads();
+    for (int s = tid; s < S; s += kPlanThreads) {
+        const int tok0 = lead_blocks[s] * B, own = ctx[s] - tok0, lead = lead_states[s];
+        const int per = part_of(own), parts = max(1, (own + per - 1) / per);
+        const unsigned i0 = per > big ? atomicAdd(&s_front, (unsigned)parts) : s_big + atomicAdd(&s_back, (unsigned)parts);
+        for (int p = 0; p < parts; ++p)
+            a.own[i0 + p] = OwnItem{s, tok0 + p * per, max(0, min(per, own - p * per)), lead, p, parts, {0, 0}};
+        if (parts > 1)
+            for (int h = 0; h < a.g.num_kv_heads; ++h) a.arrived[(size_t)s * a.g.num_kv_heads + h] = 0u;
     }
     __syncthreads();
-    const bool any = s_max > 0;
-    int pb = d.partition_blocks;
-    if (any) {
-        if (tid == 0) {
-            const int max_pb = kMaxPartitionTokens / B;
-            const double share = (double)s_tok / (double)(d.num_ctas > 0 ? d.num_ctas : 1);
-            while (2 * pb <= max_pb && pb * B < s_max && (double)min(2 * pb * B, s_max) * 4.0 <= share) pb *= 2;
-            s_pb = pb;
-        }
-        for (int i = tid; i < kMaxPartitionTokens / 16 + 1; i += kPlanThreads) bucket[i] = 0;
-        __syncthreads();
-        pb = s_pb;
-    }
-    const int P = pb * B;
-    RowInfo* info = reinterpret_cast<RowInfo*>(a.row_info);
-    for (int s = tid; s < d.num_seqs; s += kPlanThreads) {
-        const int L = long_len(s), np = (L + P - 1) / P;
-        if (np > 0) {
-            const int last = (L - (np - 1) * P + B - 1) / B;
-            if (np > 1) atomicAdd(&bucket[pb], np - 1);
-            atomicAdd(&bucket[last], 1);
-        }
-        const RowInfo r{lead_blocks[s], lead_states[s], np > 0 ? np : kDirect, ctx[s]};
-        *reinterpret_cast<int4*>(info + s) = make_int4(r.lead_blocks, r.lead_states, r.own_parts, r.L);
-    }
-    if (any) {
-        __syncthreads();
-        if (warp == 0) {
-            int running = 0;  // start of each size, largest first
-            for (int base = pb; base >= 0; base -= 32) {
-                const int sz = base - lane;
-                const int c = sz >= 0 ? bucket[sz] : 0;
-                int x = c;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, x, o);
-                    if (lane >= o) x += y;
-                }
-                if (sz >= 0) bucket[sz] = running + x - c;
-                running += __shfl_sync(0xffffffffu, x, 31);
-            }
-            if (lane == 0) d.plan[1] = (unsigned)running;
-        }
-        __syncthreads();
-        uint4* list = reinterpret_cast<uint4*>(d.plan_list);
-        for (int s = tid; s < d.num_seqs; s += kPlanThreads) {
-            const int L = long_len(s), np = (L + P - 1) / P;
-            const int last = (L - (np - 1) * P + B - 1) / B;
-            for (int p = 0; p < np; ++p) {
-                const int pos = atomicAdd(&bucket[p < np - 1 ? pb : last], 1);
-                list[pos] = make_uint4(((unsigned)s << 11) | (unsigned)p, (unsigned)ctx[s], (unsigned)lead_blocks[s],
-                                       (unsigned)lead_states[s]);
-            }
-        }
-    } else if (tid == 0) {
-        d.plan[1] = 0u;
-    }
     if (tid == 0) {
-        d.plan[0] = 0u;
-        d.plan[2] = (unsigned)pb;
-        d.plan[4] = 0u;
-        const_cast<unsigned*>(a.g.counts)[0] = s_items;
+        unsigned* counts = const_cast<unsigned*>(a.g.counts);
+        counts[0] = s_items;
+        counts[2] = s_big + s_back;
     }
 }
 
-// The finish, a CTA per (row, kv head): the row's own tokens (up to kDirectTokens of them),
-// and the join with the partial states of its shared tokens (or of its own ones, when they were
-// long).  The own tokens are read while the shared tokens' kernel still runs; only the join
-// waits for it.
+// The own tokens and the join.
 //
-// The own tokens, 16 at a time per warp, straight from global memory into the operands of
-// m16n8k16 MMAs (fp32 accumulation).  An MMA's order of k is free as long as both operands
-// agree, and so is the order of output rows, so every lane loads 16 contiguous bytes:
+// A unit is one kv head of a row, or of a part of it, and one warp's.  Thousands of them are
+// short (a sampled stream's own tokens are 1 to 40), so what counts is that no unit waits for
+// another and that the next one's bytes are under way while one ends: every warp streams its
+// units' K and V, 16 tokens a step, through a ring of its own (cp.async, swizzled as TMA's 128
+// bytes would be), and a unit's q comes with its first step.  The copies run ahead by the ring's
+// stages, across units; the units' entries and blocks are fetched ahead of that.  (With TMA boxes
+// of a block's 16 tokens the step was as long again: a thread takes 200 to 250 cycles to issue
+// one, 1,100 a step, where the step's arithmetic takes 1,000 to 1,200 and these copies 200.)
+//
+// A step's products are m16n8k16 MMAs (fp32 accumulation).  An MMA's order of k is free as long
+// as both operands agree, and so is the order of output rows, so every lane reads 16 contiguous
+// bytes at a time and nothing is transposed:
 //   S^T[heads][tokens] = q K^T: lane (g, t) holds dims 8t .. 8t+7 of each 32 for head g (A) and
 //     for tokens g and g + 8 (B);
 //   O^T[dims][heads] += V^T P: lane (g, t) holds dims 8g .. 8g+7 of each 64 for tokens 2t, 2t+1,
 //     2t+8, 2t+9; pairs of tokens are packed per dim (A), and P comes out of S^T's accumulators
 //     in B's layout as it is.  P is split into a bf16 head and remainder, as in pa_decode.
-// Small units bound this part (a sampled stream's own tokens are 1 to 40): a unit of the
-// persistent kernel costs some 3 us however small, a CTA here has all its loads in flight at once.
-constexpr int kFinThreads = 128, kFinWarps = 4;
+// Lane (g, t) ends with dims 8g .. 8g+7 of each 64 of heads 2t and 2t + 1, and reads the other
+// states of the row the same way, 32 contiguous bytes each.
+constexpr int kOwnThreads = 128, kOwnWarps = 4, kStep = 16;
+
+template <int D, int G>
+struct OwnCfg {
+    static constexpr int NH = D / 64;
+    static constexpr int HALF = kStep * 128;               // 64 columns of a step's K or V
+    static constexpr int QBYTES = G * D * 2;
+    static constexpr int STAGE = 2 * NH * HALF + (QBYTES + 1023) / 1024 * 1024;
+    static constexpr int NST = (113 * 1024 - 512) / (kOwnWarps * STAGE);  // two CTAs per SM
+    static constexpr int SMEM = kOwnWarps * NST * STAGE;
+    static_assert(NST >= 2 && 2 * (SMEM + 1024) <= 227 * 1024, "two CTAs per SM, two stages a warp");
+};
 
 __device__ __forceinline__ uint32_t lo_pair(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x5410); }
 __device__ __forceinline__ uint32_t hi_pair(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); }
 
-template <int D, int G>
-__global__ void __launch_bounds__(kFinThreads, 3) shared_finish_kernel(const SharedArgs a)
+// A warp's softmax state of one kv head.
+template <int D>
+struct OwnState {
+    static constexpr int NV = D / 64;
+    float m, l;          // head g: running maximum, and this lane's share of the sum (all of it after finish)
+    float o[NV * 4][4];  // dims 64c + 8g + j, heads 2t and 2t + 1; then dims + 4
+
+    __device__ __forceinline__ void clear()
+    {
+        m = -INFINITY;
+        l = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV * 4; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    }
+    // the output columns by a factor per head g
+    __device__ __forceinline__ void scale(float f, int t)
+    {
+        const float f0 = __shfl_sync(0xffffffffu, f, 8 * t), f1 = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+#pragma unroll
+        for (int i = 0; i < NV * 4; ++i) {
+            o[i][0] *= f0;
+            o[i][1] *= f1;
+            o[i][2] *= f0;
+            o[i][3] *= f1;
+        }
+    }
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src)
 {
-    constexpr int NC = D / 32;                         // 16-byte chunks of a K row per lane
-    constexpr int NV = D / 64;                         // and of a V row
-    __shared__ float s_o[kFinWarps][G][D];
-    __shared__ float s_inv[G];
-    extern __shared__ float s_ml[];                    // [G][states] maxima (then weights), [G][states] sums
-    const DecodeArgs& d = a.d;
-    const int max_states = kFinWarps + d.num_partitions;
-    float* s_m = s_ml;
-    float* s_l = s_ml + G * max_states;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    if (a.wait_first) pdl_wait_primary();
-    const int s = blockIdx.x / d.num_kv_heads, kvh = blockIdx.x % d.num_kv_heads;
-    const int4 ri = __ldcg(reinterpret_cast<const int4*>(a.row_info) + s);
-    const int B = a.g.block_size, lead = ri.y, parts = ri.z == kDirect ? 0 : ri.z, L = ri.w;
-    if (lead == 0 && parts == 1) return;  // one partition and nothing shared: the decode kernel wrote the row
-    const int tok0 = ri.x * B;
-    float m = -INFINITY, l = 0.f;         // head g, this lane's tokens' sum
-    float o[NV * 4][4];
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds16(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+
+// q of a unit from shared memory ([G][D]) into the A operand's registers.
+template <int D, int G>
+__device__ __forceinline__ void load_q(uint32_t qs, uint4 (&q)[D / 32])
+{
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int i = 0; i < NV * 4; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    if (ri.z == kDirect && tok0 + warp * 16 < L) {
-        const __nv_bfloat16* kc = static_cast<const __nv_bfloat16*>(d.k_cache);
-        const __nv_bfloat16* vc = static_cast<const __nv_bfloat16*>(d.v_cache);
-        const int32_t* table = d.block_tables + (size_t)s * d.max_blocks_per_seq;
-        const float sl = d.scale_log2;
-        uint4 q[NC];
-        const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(d.q) +
-                                                         ((size_t)s * d.num_heads + (size_t)kvh * G + (g < G ? g : 0)) * D);
+    for (int c = 0; c < D / 32; ++c) q[c] = g < G ? lds16(qs + g * D * 2 + c * 64 + t * 16) : make_uint4(0, 0, 0, 0);
+}
+
+// One step: 16 tokens of K at ks and of V at vs (halves of 64 columns, 128-byte swizzle), `left` of them valid.
+template <int D, int G>
+__device__ __forceinline__ void own_step(uint32_t ks, uint32_t vs, int left, float sl, const uint4 (&q)[D / 32], OwnState<D>& st)
+{
+    constexpr int NC = D / 32, NV = D / 64, HALF = kStep * 128;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    float x[2][4];
 #pragma unroll
-        for (int c = 0; c < NC; ++c) q[c] = g < G ? __ldg(qp + c * 4 + t) : make_uint4(0, 0, 0, 0);
-        int phys = __ldg(table + (tok0 + warp * 16) / B);
-        for (int tk = tok0 + warp * 16; tk < L; tk += kFinWarps * 16) {
-            if ((unsigned)phys >= (unsigned)d.num_blocks) {
-                if (lane == 0) atomicOr(d.status, PA_DEV_BAD_BLOCK);
-                phys = 0;
-            }
-            const size_t base = (((size_t)phys * d.num_kv_heads + kvh) * B + tk % B) * D;
-            const int left = L - tk;  // tokens of this step
-            uint4 k[2][NC], v[4][NV];
+    for (int n = 0; n < 2; ++n) {
+        x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.f;
+        uint4 k[NC];
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+        for (int c = 0; c < NC; ++c) {
+            const int ch = c * 4 + t;  // 16-byte chunk of the row: its half, and its place there
+            k[c] = lds16(ks + (ch >> 3) * HALF + (n * 8 + g) * 128 + (((ch & 7) ^ g) << 4));
+        }
 #pragma unroll
-                for (int c = 0; c < NC; ++c)
-                    k[n][c] = ldg_stream(reinterpret_cast<const uint4*>(kc + base + (size_t)(n * 8 + g) * D) + c * 4 + t);
+        for (int c = 0; c < NC; ++c) {
+            const uint32_t a0[4] = {q[c].x, 0u, q[c].y, 0u}, a1[4] = {q[c].z, 0u, q[c].w, 0u};
+            mma_bf16(x[n], a0, k[c].x, k[c].y);
+            mma_bf16(x[n], a1, k[c].z, k[c].w);
+        }
+    }
+    // logits of head g for tokens 2t, 2t+1, 2t+8, 2t+9
+    float y[4];
+    float mx = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int vt = 2 * t + (i & 1) + (i >> 1) * 8;
+    for (int i = 0; i < 4; ++i) {
+        const int vt = 2 * t + (i & 1) + (i >> 1) * 8;
+        y[i] = vt < left ? x[i >> 1][i & 1] * sl : -INFINITY;
+        mx = fmaxf(mx, y[i]);
+    }
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    const float mn = fmaxf(st.m, mx);
+    if (__any_sync(0xffffffffu, mn > st.m)) {
+        const float al = st.m == -INFINITY ? 0.f : exp2f(st.m - mn);
+        st.m = mn;
+        st.l *= al;
+        st.scale(al, t);
+    }
+    float p[4];
 #pragma unroll
-                for (int c = 0; c < NV; ++c)
-                    // (tokens past the context: their weight is 0, and 0 must not meet a NaN left in the pool)
-                    v[i][c] = vt < left ? ldg_stream(reinterpret_cast<const uint4*>(vc + base + (size_t)vt * D) + c * 8 + g)
-                                        : make_uint4(0, 0, 0, 0);
-            }
-            if (tk + kFinWarps * 16 < L) phys = __ldg(table + (tk + kFinWarps * 16) / B);
-            float x[2][4];
+    for (int i = 0; i < 4; ++i) {
+        p[i] = y[i] == -INFINITY ? 0.f : exp2f(y[i] - st.m);
+        st.l += p[i];
+    }
+    const uint32_t h0 = pack_bf16(p[0], p[1]), h1 = pack_bf16(p[2], p[3]);
+    const uint32_t r0 = pack_bf16(p[0] - __uint_as_float(h0 << 16), p[1] - __uint_as_float(h0 & 0xffff0000u));
+    const uint32_t r1 = pack_bf16(p[2] - __uint_as_float(h1 << 16), p[3] - __uint_as_float(h1 & 0xffff0000u));
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.f;
+    for (int c = 0; c < NV; ++c) {
+        uint32_t w[4][4];
 #pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    const uint32_t a0[4] = {q[c].x, 0u, q[c].y, 0u}, a1[4] = {q[c].z, 0u, q[c].w, 0u};
-                    mma_bf16(x[n], a0, k[n][c].x, k[n][c].y);
-                    mma_bf16(x[n], a1, k[n][c].z, k[n][c].w);
-                }
-            }
-            // logits of head g for tokens 2t, 2t+1, 2t+8, 2t+9
-            float y[4];
-            float mx = -INFINITY;
+        for (int i = 0; i < 4; ++i) {
+            const int vt = 2 * t + (i & 1) + (i >> 1) * 8;
+            // (tokens past the context: their weight is 0, and 0 must not meet a NaN left in the pool)
+            const uint4 v = vt < left ? lds16(vs + c * HALF + vt * 128 + ((g ^ (vt & 7)) << 4)) : make_uint4(0, 0, 0, 0);
+            w[i][0] = v.x;
+            w[i][1] = v.y;
+            w[i][2] = v.z;
+            w[i][3] = v.w;
+        }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int vt = 2 * t + (i & 1) + (i >> 1) * 8;
-                y[i] = vt < left ? x[i >> 1][i & 1] * sl : -INFINITY;
-                mx = fmaxf(mx, y[i]);
-            }
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const float mn = fmaxf(m, mx);
-            if (__any_sync(0xffffffffu, mn > m)) {
-                const float al = m == -INFINITY ? 0.f : exp2f(m - mn);
-                m = mn;
-                l *= al;
-                // heads 2t and 2t + 1 of the output columns
-                const float al0 = __shfl_sync(0xffffffffu, al, 8 * t), al1 = __shfl_sync(0xffffffffu, al, 8 * t + 4);
-#pragma unroll
-                for (int i = 0; i < NV * 4; ++i) {
-                    o[i][0] *= al0;
-                    o[i][1] *= al1;
-                    o[i][2] *= al0;
-                    o[i][3] *= al1;
-                }
-            }
-            float p[4];
+        for (int j = 0; j < 4; ++j) {
+            // output rows g: dim 8g + j, rows g + 8: dim 8g + j + 4 (of 64)
+            const int e = j >> 1;
+            uint32_t af[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                p[i] = y[i] == -INFINITY ? 0.f : exp2f(y[i] - m);
-                l += p[i];
+                const uint32_t x0 = w[(i >> 1) * 2][e + (i & 1) * 2], x1 = w[(i >> 1) * 2 + 1][e + (i & 1) * 2];
+                af[i] = (j & 1) ? hi_pair(x0, x1) : lo_pair(x0, x1);
             }
-            const uint32_t h0 = pack_bf16(p[0], p[1]), h1 = pack_bf16(p[2], p[3]);
-            const uint32_t r0 = pack_bf16(p[0] - __uint_as_float(h0 << 16), p[1] - __uint_as_float(h0 & 0xffff0000u));
-            const uint32_t r1 = pack_bf16(p[2] - __uint_as_float(h1 << 16), p[3] - __uint_as_float(h1 & 0xffff0000u));
+            mma_bf16(st.o[c * 4 + j], af, h0, h1);
+            mma_bf16(st.o[c * 4 + j], af, r0, r1);
+        }
+    }
+}
+
+// Adds the states slot(first), slot(first + step), ... (below n) of the row and kv head to the warp's.  The
+// output columns of heads G and up are nobody's, so their lanes take states of their own: 4 / HP at a time.
+template <int D, int G, class Slot>
+__device__ __forceinline__ void absorb_states(const SharedArgs& a, size_t row0, OwnState<D>& st, int n, int first, int step,
+                                              Slot slot)
+{
+    constexpr int NV = D / 64, HP = G >= 2 ? G / 2 : 1, SPL = 4 / HP;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int hp = t % HP, sub = t / HP;
+    const int np = a.g.num_partitions;
+    const int cnt = (n - first + step - 1) / step;
+    if (cnt <= 0) return;
+    const float2* ml = reinterpret_cast<const float2*>(a.g.ws_ml) + row0 * np;
+    float M = st.m;
+    for (int i = t; i < cnt; i += 4) M = fmaxf(M, __ldcg(ml + (size_t)(g < G ? g : 0) * np + slot(first + i * step)).x);
+    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 1));
+    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 2));
+    const float f = st.m == -INFINITY ? 0.f : exp2f(st.m - M);
+    st.m = M;
+    st.l *= f;
+    st.scale(f, t);
+    if (t >= HP) {
+#pragma unroll
+        for (int i = 0; i < NV * 4; ++i) st.o[i][0] = st.o[i][1] = st.o[i][2] = st.o[i][3] = 0.f;
+    }
+    const float M0 = __shfl_sync(0xffffffffu, M, 8 * hp), M1 = __shfl_sync(0xffffffffu, M, 8 * hp + 4);
+    float l0 = 0.f, l1 = 0.f;
+    for (int i = 0; i < cnt; i += SPL) {
+        const bool valid = i + sub < cnt;
+        const int p = slot(first + min(i + sub, cnt - 1) * step);
+        const float4* acc = reinterpret_cast<const float4*>(a.g.ws_acc + ((row0 + 2 * hp) * np + p) * D + 8 * g);
+        float4 x[G >= 2 ? 2 : 1][NV][2];
+        float2 v[2];
+#pragma unroll
+        for (int h = 0; h < (G >= 2 ? 2 : 1); ++h) {
+            v[h] = __ldcg(ml + (size_t)(2 * hp + h) * np + p);
 #pragma unroll
             for (int c = 0; c < NV; ++c) {
-                const uint32_t* w[4] = {&v[0][c].x, &v[1][c].x, &v[2][c].x, &v[3][c].x};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    // output rows g: dim 8g + j, rows g + 8: dim 8g + j + 4 (of 64)
-                    const int e = j >> 1;
-                    uint32_t af[4];
-                    if (j & 1) {
-                        af[0] = hi_pair(w[0][e], w[1][e]);
-                        af[1] = hi_pair(w[0][e + 2], w[1][e + 2]);
-                        af[2] = hi_pair(w[2][e], w[3][e]);
-                        af[3] = hi_pair(w[2][e + 2], w[3][e + 2]);
-                    } else {
-                        af[0] = lo_pair(w[0][e], w[1][e]);
-                        af[1] = lo_pair(w[0][e + 2], w[1][e + 2]);
-                        af[2] = lo_pair(w[2][e], w[3][e]);
-                        af[3] = lo_pair(w[2][e + 2], w[3][e + 2]);
-                    }
-                    mma_bf16(o[c * 4 + j], af, h0, h1);
-                    mma_bf16(o[c * 4 + j], af, r0, r1);
-                }
+                x[h][c][0] = __ldcg(acc + (size_t)h * np * (D / 4) + c * 16);
+                x[h][c][1] = __ldcg(acc + (size_t)h * np * (D / 4) + c * 16 + 1);
             }
         }
-        l += __shfl_xor_sync(0xffffffffu, l, 1);
-        l += __shfl_xor_sync(0xffffffffu, l, 2);
-    }
-    // the warps' states to shared memory
-    if (t == 0 && g < G) {
-        s_m[g * max_states + warp] = m;
-        s_l[g * max_states + warp] = l;
-    }
 #pragma unroll
-    for (int i = 0; i < NV * 4; ++i) {
-        const int dim = (i >> 2) * 64 + 8 * g + (i & 3);
-        if (2 * t < G) {
-            s_o[warp][2 * t][dim] = o[i][0];
-            s_o[warp][2 * t][dim + 4] = o[i][2];
-        }
-        if (2 * t + 1 < G) {
-            s_o[warp][2 * t + 1][dim] = o[i][1];
-            s_o[warp][2 * t + 1][dim + 4] = o[i][3];
-        }
-    }
-    // everything else the row's states need is written from here on
-    if (!a.wait_first) pdl_wait_primary();
-    const int nst = kFinWarps + lead + parts;
-    const size_t row0 = (size_t)s * d.num_heads + (size_t)kvh * G;
-    auto slot = [&](int p) { return p < lead ? p : d.lead_partitions + p - lead; };
-    for (int i = threadIdx.x; i < G * (lead + parts); i += kFinThreads) {
-        const int h = i / (lead + parts), p = i % (lead + parts);
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(d.ws_ml) + (row0 + h) * d.num_partitions + slot(p));
-        s_m[h * max_states + kFinWarps + p] = ml.x;
-        s_l[h * max_states + kFinWarps + p] = ml.y;
-    }
-    __syncthreads();
-    for (int h = warp; h < G; h += kFinWarps) {
-        float M = -INFINITY, den = 0.f;
-        for (int i = lane; i < nst; i += 32) M = fmaxf(M, s_m[h * max_states + i]);
+        for (int h = 0; h < (G >= 2 ? 2 : 1); ++h) {
+            const float w = valid ? exp2f(v[h].x - (h ? M1 : M0)) : 0.f;
+            if (h) l1 = fmaf(w, v[h].y, l1);
+            else l0 = fmaf(w, v[h].y, l0);
 #pragma unroll
-        for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-        for (int i = lane; i < nst; i += 32) {
-            const float mi = s_m[h * max_states + i], w = mi == -INFINITY ? 0.f : exp2f(mi - M);
-            s_m[h * max_states + i] = w;
-            den = fmaf(w, s_l[h * max_states + i], den);
-        }
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) den += __shfl_xor_sync(0xffffffffu, den, x);
-        if (lane == 0) s_inv[h] = den > 0.f ? 1.f / den : 0.f;
-    }
-    __syncthreads();
-    // two columns a thread
-    constexpr int TPH = D / 2;
-    for (int h = threadIdx.x / TPH; h < G; h += kFinThreads / TPH) {
-        const int col = (threadIdx.x % TPH) * 2;
-        float n0 = 0.f, n1 = 0.f;
-#pragma unroll
-        for (int w = 0; w < kFinWarps; ++w) {
-            const float wt = s_m[h * max_states + w];
-            if (wt != 0.f) {
-                n0 = fmaf(wt, s_o[w][h][col], n0);
-                n1 = fmaf(wt, s_o[w][h][col + 1], n1);
+            for (int c = 0; c < NV; ++c) {
+                const float4 lo = x[h][c][0], hi = x[h][c][1];
+                st.o[c * 4 + 0][h] = fmaf(w, lo.x, st.o[c * 4 + 0][h]);
+                st.o[c * 4 + 1][h] = fmaf(w, lo.y, st.o[c * 4 + 1][h]);
+                st.o[c * 4 + 2][h] = fmaf(w, lo.z, st.o[c * 4 + 2][h]);
+                st.o[c * 4 + 3][h] = fmaf(w, lo.w, st.o[c * 4 + 3][h]);
+                st.o[c * 4 + 0][h + 2] = fmaf(w, hi.x, st.o[c * 4 + 0][h + 2]);
+                st.o[c * 4 + 1][h + 2] = fmaf(w, hi.y, st.o[c * 4 + 1][h + 2]);
+                st.o[c * 4 + 2][h + 2] = fmaf(w, hi.z, st.o[c * 4 + 2][h + 2]);
+                st.o[c * 4 + 3][h + 2] = fmaf(w, hi.w, st.o[c * 4 + 3][h + 2]);
             }
         }
-        const float* acc = d.ws_acc + (row0 + h) * d.num_partitions * D + col;
-        for (int p0 = 0; p0 < lead + parts; p0 += 8) {
-            float2 x[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                x[i] = __ldcg(reinterpret_cast<const float2*>(acc + (size_t)slot(min(p0 + i, lead + parts - 1)) * D));
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float wt = p0 + i < lead + parts ? s_m[h * max_states + kFinWarps + p0 + i] : 0.f;
-                if (wt != 0.f) {
-                    n0 = fmaf(wt, x[i].x, n0);
-                    n1 = fmaf(wt, x[i].y, n1);
-                }
-            }
-        }
-        *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(d.out) + (row0 + h) * D + col) =
-            pack_bf16(n0 * s_inv[h], n1 * s_inv[h]);
     }
+#pragma unroll
+    for (int x = HP; x < 4; x <<= 1) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, x);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, x);
+#pragma unroll
+        for (int i = 0; i < NV * 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) st.o[i][e] += __shfl_xor_sync(0xffffffffu, st.o[i][e], x);
+    }
+    // the sums belong with head g: lane t = (g / 2) has them for heads 2t and 2t + 1
+    const float s0 = __shfl_sync(0xffffffffu, l0, (g >> 1) % HP), s1 = __shfl_sync(0xffffffffu, l1, (g >> 1) % HP);
+    st.l += (g & 1) ? s1 : s0;
 }
 
-template <class Cons, int BS>
-cudaError_t launch_shared_c(const SharedArgs& a, int group, cudaStream_t stream)
+template <int D, int G>
+__device__ __forceinline__ void write_row(const SharedArgs& a, size_t row0, OwnState<D>& st)
 {
-    using P = Persist<Cons, BS>;
-    CUtensorMap tk, tv;
-    std::memset(&tk, 0, sizeof(tk));
-    std::memset(&tv, 0, sizeof(tv));
-    cudaError_t e;
-    if constexpr (Cons::kTensorLoads) {
-        const uint64_t rows = (uint64_t)a.d.num_blocks * a.d.num_kv_heads * BS;
-        if ((e = encode_pool_map(&tk, a.d.k_cache, rows, P::D, P::TR)) != cudaSuccess) return e;
-        if ((e = encode_pool_map(&tv, a.d.v_cache, rows, P::D, P::TR)) != cudaSuccess) return e;
+    constexpr int NV = D / 64;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    st.scale(st.l > 0.f ? 1.f / st.l : 0.f, t);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        if (2 * t + h < G) {
+            uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.g.out) + (row0 + 2 * t + h) * D + 8 * g);
+#pragma unroll
+            for (int c = 0; c < NV; ++c) {
+                uint4 pk;
+                pk.x = pack_bf16(st.o[c * 4 + 0][h], st.o[c * 4 + 1][h]);
+                pk.y = pack_bf16(st.o[c * 4 + 2][h], st.o[c * 4 + 3][h]);
+                pk.z = pack_bf16(st.o[c * 4 + 0][h + 2], st.o[c * 4 + 1][h + 2]);
+                pk.w = pack_bf16(st.o[c * 4 + 2][h + 2], st.o[c * 4 + 3][h + 2]);
+                out[c * 8] = pk;
+            }
+        }
+}
+
+template <int D, int G>
+__global__ void __launch_bounds__(kOwnThreads, 2) shared_own_kernel(const __grid_constant__ SharedArgs a)
+{
+    using C = OwnCfg<D, G>;
+    constexpr int NV = D / 64, NST = C::NST, CPR = D / 8;  // 16-byte chunks of a row
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const unsigned Hkv = (unsigned)a.g.num_kv_heads;
+    const uint32_t ring = smem_u32(smem) + warp * NST * C::STAGE;
+    if (a.wait_first) pdl_wait_primary();
+    const unsigned entries = __ldcg(a.g.counts + 2), total = entries * Hkv;
+    const unsigned first = blockIdx.x * kOwnWarps + warp, hop = gridDim.x * kOwnWarps;
+
+    // The copying cursor: unit iu at token itk, the block of that step, and the entry of the unit after.
+    auto table_at = [&](const OwnItem& it, int tk) {
+        return it.ntok > 0 ? __ldg(a.g.block_tables + (size_t)it.row * a.g.max_blocks_per_seq + tk / a.g.block_size) : 0;
+    };
+    unsigned iu = first;
+    OwnItem icur = load_own(a.own, iu / Hkv, iu < total ? entries : 0u);
+    OwnItem inext = load_own(a.own, (iu + hop) / Hkv, iu + hop < total ? entries : 0u);
+    int itk = icur.tok0, iphys = table_at(icur, itk), ist = 0;
+    // lane's chunk of rows lane / CPR, + 32 / CPR, ...: the swizzle repeats every 8 rows
+    constexpr int RPI = 32 / CPR;
+    const int crow = lane / CPR, cch = lane % CPR;
+    auto issue = [&]() {
+        if (iu < total) {
+            const int kvh = (int)(iu % Hkv);
+            const uint32_t dst = ring + ist * C::STAGE;
+            if (icur.ntok > 0) {
+                int phys = iphys;
+                if ((unsigned)phys >= (unsigned)a.g.num_blocks) {
+                    if (lane == 0) atomicOr(a.g.status, PA_DEV_BAD_BLOCK);
+                    phys = 0;
+                }
+                const size_t off = ((((size_t)phys * Hkv + kvh) * a.g.block_size + itk % a.g.block_size) * D) * 2 + lane * 16;
+                const char* kp = static_cast<const char*>(a.g.k_cache) + off;
+                const char* vp = static_cast<const char*>(a.g.v_cache) + off;
+#pragma unroll
+                for (int i = 0; i < kStep / RPI; ++i) {
+                    const int r = crow + i * RPI;
+                    const uint32_t d = dst + (cch >> 3) * C::HALF + r * 128 + (((cch & 7) ^ (r & 7)) << 4);
+                    cp_async16(d, kp + i * 512);
+                    cp_async16(d + C::NH * C::HALF, vp + i * 512);
+                }
+                if (itk == icur.tok0) {
+                    const char* qp = static_cast<const char*>(a.g.q) +
+                                     ((size_t)icur.row * a.g.num_heads + (size_t)kvh * G) * (D * 2);
+#pragma unroll
+                    for (int i = 0; i < (G * CPR + 31) / 32; ++i)
+                        if (i * 32 + lane < G * CPR)
+                            cp_async16(dst + 2 * C::NH * C::HALF + (i * 32 + lane) * 16, qp + (i * 32 + lane) * 16);
+                }
+            }
+            // on to the next step (a unit without tokens takes one, without bytes): its block is asked for now
+            if (itk + kStep < icur.tok0 + icur.ntok) {
+                itk += kStep;
+            } else {
+                iu += hop;
+                icur = inext;
+                inext = load_own(a.own, (iu + hop) / Hkv, iu + hop < total ? entries : 0u);
+                itk = icur.tok0;
+            }
+            iphys = table_at(icur, itk);
+        }
+        ist = ist + 1 == NST ? 0 : ist + 1;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll 1
+    for (int i = 0; i < NST; ++i) issue();
+
+    bool waited = a.wait_first != 0;
+    int sg = 0;  // stage of the next step
+    OwnState<D> st;
+    OwnItem it = load_own(a.own, first / Hkv, first < total ? entries : 0u);
+    for (unsigned u = first; u < total; u += hop) {
+        const OwnItem next = load_own(a.own, (u + hop) / Hkv, u + hop < total ? entries : 0u);
+        const int kvh = (int)(u % Hkv);
+        const size_t row0 = (size_t)it.row * a.g.num_heads + (size_t)kvh * G;
+        st.clear();
+        uint4 q[D / 32];
+        const int n = max(1, (it.ntok + kStep - 1) / kStep);
+        for (int j = 0; j < n; ++j) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(NST - 1) : "memory");
+            __syncwarp();
+            const uint32_t base = ring + sg * C::STAGE;
+            if (it.ntok > 0) {
+                if (j == 0) load_q<D, G>(base + 2 * C::NH * C::HALF, q);
+                own_step<D, G>(base, base + C::NH * C::HALF, it.ntok - j * kStep, a.g.scale_log2, q, st);
+            }
+            __syncwarp();  // every lane has read the stage
+            sg = sg + 1 == NST ? 0 : sg + 1;
+            issue();
+        }
+        st.l += __shfl_xor_sync(0xffffffffu, st.l, 1);
+        st.l += __shfl_xor_sync(0xffffffffu, st.l, 2);
+        bool last = true;
+        if (it.parts > 1) {
+            // this part's state; the last part of the row and kv head to get here joins them all, in order
+            const int np = a.g.num_partitions, sl = a.g.lead_partitions + it.part;
+            if (t == 0 && g < G)
+                *reinterpret_cast<float2*>(a.g.ws_ml + ((row0 + g) * np + sl) * 2) = make_float2(st.m, st.l);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (2 * t + h < G) {
+                    float4* acc = reinterpret_cast<float4*>(a.g.ws_acc + ((row0 + 2 * t + h) * np + sl) * D + 8 * g);
+#pragma unroll
+                    for (int c = 0; c < NV; ++c) {
+                        acc[c * 16] = make_float4(st.o[c * 4][h], st.o[c * 4 + 1][h], st.o[c * 4 + 2][h], st.o[c * 4 + 3][h]);
+                        acc[c * 16 + 1] =
+                            make_float4(st.o[c * 4][h + 2], st.o[c * 4 + 1][h + 2], st.o[c * 4 + 2][h + 2], st.o[c * 4 + 3][h + 2]);
+                    }
+                }
+            __threadfence();
+            __syncwarp();
+            unsigned before = 0;
+            if (lane == 0) before = atomicAdd(a.arrived + (size_t)it.row * Hkv + kvh, 1u);
+            before = __shfl_sync(0xffffffffu, before, 0);
+            __threadfence();
+            last = before == (unsigned)it.parts - 1;
+            if (last) st.clear();
+        }
+        if (last) {
+            if (it.lead > 0 && !waited) {
+                pdl_wait_primary();  // the shared tokens' states
+                waited = true;
+            }
+            const int lead = it.lead, skip = a.g.lead_partitions - lead;
+            absorb_states<D, G>(a, row0, st, lead + (it.parts > 1 ? it.parts : 0), 0, 1,
+                                [lead, skip](int p) { return p < lead ? p : p + skip; });
+            write_row<D, G>(a, row0, st);
+        }
+        it = next;
     }
-    int ctas = 0;
-    if ((e = resident_ctas<Cons, BS, kModeOwn>(&ctas)) != cudaSuccess) return e;
-    const int64_t units = (int64_t)a.d.num_kv_heads * a.d.num_seqs * (a.d.num_partitions - a.d.lead_partitions);
-    const unsigned grid = (unsigned)(units < ctas ? units : ctas);
-    SharedArgs args = a;
-    args.d.num_ctas = (int)grid;
-    const bool shares = a.g.max_entries > 0;
-    args.d.wait_first = shares ? 0 : 1;
+    // whatever waits for this grid may count on the shared tokens' kernel having finished too
+    if (!waited) pdl_wait_primary();
+}
+
+template <int D, int G>
+cudaError_t launch_shared_dg(const SharedArgs& a, cudaStream_t stream)
+{
+    using C = OwnCfg<D, G>;
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const int tile_rows = shared_tile_rows(a.num_groups, a.num_group_rows, group);
-    const int gctas = group_resident_ctas(sms);
-    shared_plan_kernel<<<1, kPlanThreads, 0, stream>>>(args, tile_rows / group, gctas);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if (shares && (e = launch_group(args.g, P::D, group, tile_rows, gctas, stream)) != cudaSuccess) return e;
-    // without a context longer than kDirectTokens the finish has every own token
-    const bool longs = a.d.max_context_len > kDirectTokens;
-    if (longs) {
-        e = launch_pdl(decode_persistent_kernel<Cons, BS, kModeOwn>, dim3(grid), dim3(P::THREADS), (size_t)P::SMEM,
-                       stream, args.d, tk, tv);
-        if (e != cudaSuccess) return e;
-    }
-    args.wait_first = shares ? 0 : 1;
-    const size_t smem = 2 * sizeof(float) * P::G * (size_t)(kFinWarps + a.d.num_partitions);
-    e = cudaFuncSetAttribute(shared_finish_kernel<P::D, P::G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(shared_own_kernel<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    return launch_pdl(shared_finish_kernel<P::D, P::G>, dim3((unsigned)(a.d.num_seqs * a.d.num_kv_heads)),
-                      dim3(kFinThreads), smem, stream, args);
+    const int tile_rows = shared_tile_rows(a.num_groups, a.num_group_rows, G);
+    const int gctas = group_resident_ctas(sms);
+    const bool shares = a.g.max_entries > 0;
+    SharedArgs args = a;
+    args.wait_first = shares ? 0 : 1;
+    const int64_t units = (int64_t)a.num_seqs * a.max_parts * a.g.num_kv_heads;
+    const unsigned grid = (unsigned)std::min<int64_t>((units + kOwnWarps - 1) / kOwnWarps, 2LL * sms);
+    shared_plan_kernel<<<1, kPlanThreads, 0, stream>>>(args, tile_rows / G, gctas, 2 * sms * kOwnWarps);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (shares && (e = launch_group(args.g, D, G, tile_rows, gctas, stream)) != cudaSuccess) return e;
+    return launch_pdl(shared_own_kernel<D, G>, dim3(grid), dim3(kOwnThreads), (size_t)C::SMEM, stream, args);
 }
 
-template <int D, int BS>
-cudaError_t launch_shared_db(const SharedArgs& a, int group, cudaStream_t stream)
+template <int D>
+cudaError_t launch_shared_d(const SharedArgs& a, int group, cudaStream_t stream)
 {
     switch (group) {
-        case 1: return launch_shared_c<FmaConsumer<__nv_bfloat16, D, 16, 1>, BS>(a, group, stream);
-        case 2: return launch_shared_c<MmaConsumer<D, 16, 2>, BS>(a, group, stream);
-        case 4: return launch_shared_c<MmaConsumer<D, 16, 4>, BS>(a, group, stream);
-        case 8: return launch_shared_c<MmaConsumer<D, 16, 8>, BS>(a, group, stream);
+        case 1: return launch_shared_dg<D, 1>(a, stream);
+        case 2: return launch_shared_dg<D, 2>(a, stream);
+        case 4: return launch_shared_dg<D, 4>(a, stream);
+        case 8: return launch_shared_dg<D, 8>(a, stream);
         default: return cudaErrorInvalidValue;
     }
 }
 
 }  // namespace
 
-cudaError_t launch_shared(const SharedArgs& a, int head_dim, int block_size, int group, cudaStream_t stream)
+cudaError_t launch_shared(const SharedArgs& a, int head_dim, int group, cudaStream_t stream)
 {
-    if (head_dim == 64)
-        return block_size == 16 ? launch_shared_db<64, 16>(a, group, stream) : launch_shared_db<64, 32>(a, group, stream);
-    return block_size == 16 ? launch_shared_db<128, 16>(a, group, stream) : launch_shared_db<128, 32>(a, group, stream);
+    return head_dim == 64 ? launch_shared_d<64>(a, group, stream) : launch_shared_d<128>(a, group, stream);
 }
 
 }  // namespace pa

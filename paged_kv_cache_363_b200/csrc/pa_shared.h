@@ -1,41 +1,53 @@
 // Launch interface of pa_decode_shared (pa_shared.cu).
 #pragma once
 
+#include <algorithm>
+
 #include "pa_group.cuh"
 #include "pa_internal.h"
 
 namespace pa {
 
+// Own tokens of one row: all of them, or one of several parts.
+struct OwnItem {
+    int row;
+    int tok0, ntok;
+    int lead;         // partial states of the row's shared tokens
+    int part, parts;
+    int pad[2];
+};
+
 struct SharedArgs {
-    GroupArgs g;               // the shared tokens' kernel and the merge
-    DecodeArgs d;              // the own tokens' kernel; plan_list has uint4 entries
+    GroupArgs g;               // the shared tokens' kernel; counts: [0] its entries, [2] those of the own tokens
+    const int32_t* context_lens;
     const int32_t* group_rows;
     const int32_t* group_start;
     const int32_t* shared_lens;
-    void* row_info;            // [S] 16 bytes: what the plan says about a row
+    OwnItem* own;              // [S * max_parts] rows' own tokens, in parts
+    unsigned* arrived;         // [S * Hkv] parts of a row and kv head that are done
     int* listed;               // [S] times a row is listed (this and the next three: batches over 1024 rows)
     int* ctx;                  // [S] context length
     int* lead_blocks;          // [S] shared blocks of a row
     int* lead_states;          // [S] partial states of its shared tokens
     int* group_ok;             // [groups]
+    int num_seqs;
     int num_groups;
     int num_group_rows;
+    int max_context_len;
     int max_shared_len;
-    int max_chunks;
-    int wait_first;            // the finish has to wait for the plan itself before it begins
+    int max_chunks;            // of the shared tokens
+    int max_parts;             // of a row's own tokens
+    int wait_first;            // the own tokens' kernel follows the plan itself
 };
 
-// Own tokens that the finish reads itself: up to eight steps of its four warps.  Longer rows are
-// split into partitions that several CTAs share.
-constexpr int kDirectTokens = 512;
-
-// Own tokens per partition at least: 512, doubled until a row has at most 16 partitions (a
-// partial state per partition is kept for every row) or a partition is as long as it may be.
-inline int shared_partition(int64_t max_context)
+// Most parts of a row's own tokens (the workspace has a partial state per part of every row): as many as
+// make four units per warp of the device (about 4,800), and where contexts are long, up to 32 of 1024
+// tokens or more; none below 256 tokens.
+inline int shared_max_parts(int64_t seqs, int64_t num_kv_heads, int64_t max_context)
 {
-    int p = 512;
-    while (p < kMaxPartitionTokens && (max_context + p - 1) / p > 16) p *= 2;
-    return p;
+    const int64_t want = (4800 + seqs * num_kv_heads - 1) / (seqs * num_kv_heads);
+    const int64_t lengthy = std::min<int64_t>(32, (max_context + 1023) / 1024);
+    return (int)std::max<int64_t>(1, std::min<int64_t>((max_context + 255) / 256, std::max(std::min<int64_t>(want, 32), lengthy)));
 }
 
 // Rows of a tile: 64 where the groups have that many rows or fewer on average (half the shared
@@ -47,7 +59,7 @@ inline int shared_tile_rows(int64_t groups, int64_t rows, int group)
 
 struct SharedWorkspace {
     GroupWorkspace g;
-    size_t entries, plan, list, row_info, listed, ctx, lead_blocks, lead_states, group_ok, acc, ml, total;
+    size_t entries, own, arrived, listed, ctx, lead_blocks, lead_states, group_ok, acc, ml, total;
     int chunks, parts;
 };
 
@@ -57,15 +69,15 @@ inline SharedWorkspace shared_workspace(size_t S, size_t Hq, int Hkv, int D, int
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     SharedWorkspace w{};
     const int G = (int)(Hq / (size_t)Hkv);
-    const int P = shared_partition(max_context);
     w.chunks = group_max_chunks(max_shared, (int64_t)rows, G, Hkv);
-    w.parts = max_context > 0 ? (max_context + P - 1) / P : 1;
-    w.entries = max_shared > 0 && rows > 0 ? (groups + rows / (size_t)(shared_tile_rows((int64_t)groups, (int64_t)rows, G) / G)) * (size_t)w.chunks : 0;
+    w.parts = shared_max_parts((int64_t)S, Hkv, max_context);
+    w.entries = max_shared > 0 && rows > 0 && groups > 0
+                    ? (groups + rows / (size_t)(shared_tile_rows((int64_t)groups, (int64_t)rows, G) / G)) * (size_t)w.chunks
+                    : 0;
     w.g = group_workspace(0, w.entries, 0);
-    w.plan = w.g.end;
-    w.list = w.plan + 256;
-    w.row_info = up(w.list + 16 * S * (size_t)w.parts);
-    w.listed = up(w.row_info + 16 * S);
+    w.own = w.g.end;
+    w.arrived = up(w.own + sizeof(OwnItem) * S * (size_t)w.parts);
+    w.listed = up(w.arrived + 4 * S * (size_t)Hkv);
     w.ctx = up(w.listed + 4 * S);
     w.lead_blocks = up(w.ctx + 4 * S);
     w.lead_states = up(w.lead_blocks + 4 * S);
@@ -77,6 +89,6 @@ inline SharedWorkspace shared_workspace(size_t S, size_t Hq, int Hkv, int D, int
     return w;
 }
 
-cudaError_t launch_shared(const SharedArgs& a, int head_dim, int block_size, int group, cudaStream_t stream);
+cudaError_t launch_shared(const SharedArgs& a, int head_dim, int group, cudaStream_t stream);
 
 }  // namespace pa

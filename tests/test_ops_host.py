@@ -99,8 +99,7 @@ def _shared(out=P, q=P, rows=P, start=P, lens=P, S=8, Hq=4, Hkv=4, D=128, B=16, 
     (dict(Hq=6), "INVALID"), (dict(nr=9), "INVALID"), (dict(ng=-1), "INVALID"), (dict(sh=-1), "INVALID"),
     (dict(rows=None), "INVALID"), (dict(start=None), "INVALID"), (dict(lens=None), "INVALID"), (dict(q=ODD), "INVALID"),
     (dict(scale=float("nan")), "INVALID"), (dict(ws=None), "INVALID"), (dict(nbytes=64), "INVALID"),
-    (dict(S=65536), "INVALID"), (dict(mb=0), "INVALID"), (dict(NB=1 << 26), "UNSUPPORTED"),
-    (dict(ctx=2048 * 4096 + 1), "UNSUPPORTED")])
+    (dict(S=65536), "INVALID"), (dict(mb=0), "INVALID"), (dict(NB=1 << 26), "UNSUPPORTED")])
 def test_decode_shared_refusals(bad, code):
     assert _shared(**bad) == getattr(pa, "PA_ERR_" + code)
     assert "pa_decode_shared" in pa.lib.pa_last_error_string().decode()
