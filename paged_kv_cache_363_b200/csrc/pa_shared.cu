@@ -246,6 +246,13 @@ struct OwnState {
     }
 };
 
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -273,37 +280,55 @@ __device__ __forceinline__ void own_step(uint32_t ks, uint32_t vs, int left, flo
 {
     constexpr int NC = D / 32, NV = D / 64, HALF = kStep * 128;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    float x[2][4];
+    // (two chains of MMAs for each half of the tokens: the step is bound by its latency)
+    float x[2][4], x2[2][4];
+    uint4 k[2][NC];
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
         x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.f;
-        uint4 k[NC];
+        x2[n][0] = x2[n][1] = x2[n][2] = x2[n][3] = 0.f;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             const int ch = c * 4 + t;  // 16-byte chunk of the row: its half, and its place there
-            k[c] = lds16(ks + (ch >> 3) * HALF + (n * 8 + g) * 128 + (((ch & 7) ^ g) << 4));
-        }
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            const uint32_t a0[4] = {q[c].x, 0u, q[c].y, 0u}, a1[4] = {q[c].z, 0u, q[c].w, 0u};
-            mma_bf16(x[n], a0, k[c].x, k[c].y);
-            mma_bf16(x[n], a1, k[c].z, k[c].w);
+            k[n][c] = lds16(ks + (ch >> 3) * HALF + (n * 8 + g) * 128 + (((ch & 7) ^ g) << 4));
         }
     }
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const uint32_t a0[4] = {q[c].x, 0u, q[c].y, 0u}, a1[4] = {q[c].z, 0u, q[c].w, 0u};
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            mma_bf16(x[n], a0, k[n][c].x, k[n][c].y);
+            mma_bf16(x2[n], a1, k[n][c].z, k[n][c].w);
+        }
+    }
+    uint32_t w[NV][4][4];
+#pragma unroll
+    for (int c = 0; c < NV; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int vt = 2 * t + (i & 1) + (i >> 1) * 8;
+            // (tokens past the context: their weight is 0, and 0 must not meet a NaN left in the pool)
+            const uint4 v = vt < left ? lds16(vs + c * HALF + vt * 128 + ((g ^ (vt & 7)) << 4)) : make_uint4(0, 0, 0, 0);
+            w[c][i][0] = v.x;
+            w[c][i][1] = v.y;
+            w[c][i][2] = v.z;
+            w[c][i][3] = v.w;
+        }
     // logits of head g for tokens 2t, 2t+1, 2t+8, 2t+9
     float y[4];
     float mx = -INFINITY;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int vt = 2 * t + (i & 1) + (i >> 1) * 8;
-        y[i] = vt < left ? x[i >> 1][i & 1] * sl : -INFINITY;
+        y[i] = vt < left ? (x[i >> 1][i & 1] + x2[i >> 1][i & 1]) * sl : -INFINITY;
         mx = fmaxf(mx, y[i]);
     }
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     const float mn = fmaxf(st.m, mx);
     if (__any_sync(0xffffffffu, mn > st.m)) {
-        const float al = st.m == -INFINITY ? 0.f : exp2f(st.m - mn);
+        const float al = st.m == -INFINITY ? 0.f : ex2(st.m - mn);
         st.m = mn;
         st.l *= al;
         st.scale(al, t);
@@ -311,7 +336,7 @@ __device__ __forceinline__ void own_step(uint32_t ks, uint32_t vs, int left, flo
     float p[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        p[i] = y[i] == -INFINITY ? 0.f : exp2f(y[i] - st.m);
+        p[i] = y[i] == -INFINITY ? 0.f : ex2(y[i] - st.m);
         st.l += p[i];
     }
     const uint32_t h0 = pack_bf16(p[0], p[1]), h1 = pack_bf16(p[2], p[3]);
@@ -319,17 +344,6 @@ __device__ __forceinline__ void own_step(uint32_t ks, uint32_t vs, int left, flo
     const uint32_t r1 = pack_bf16(p[2] - __uint_as_float(h1 << 16), p[3] - __uint_as_float(h1 & 0xffff0000u));
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
-        uint32_t w[4][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int vt = 2 * t + (i & 1) + (i >> 1) * 8;
-            // (tokens past the context: their weight is 0, and 0 must not meet a NaN left in the pool)
-            const uint4 v = vt < left ? lds16(vs + c * HALF + vt * 128 + ((g ^ (vt & 7)) << 4)) : make_uint4(0, 0, 0, 0);
-            w[i][0] = v.x;
-            w[i][1] = v.y;
-            w[i][2] = v.z;
-            w[i][3] = v.w;
-        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             // output rows g: dim 8g + j, rows g + 8: dim 8g + j + 4 (of 64)
@@ -337,7 +351,7 @@ __device__ __forceinline__ void own_step(uint32_t ks, uint32_t vs, int left, flo
             uint32_t af[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t x0 = w[(i >> 1) * 2][e + (i & 1) * 2], x1 = w[(i >> 1) * 2 + 1][e + (i & 1) * 2];
+                const uint32_t x0 = w[c][(i >> 1) * 2][e + (i & 1) * 2], x1 = w[c][(i >> 1) * 2 + 1][e + (i & 1) * 2];
                 af[i] = (j & 1) ? hi_pair(x0, x1) : lo_pair(x0, x1);
             }
             mma_bf16(st.o[c * 4 + j], af, h0, h1);
@@ -456,20 +470,20 @@ __global__ void __launch_bounds__(kOwnThreads, 2) shared_own_kernel(const __grid
     const unsigned entries = __ldcg(a.g.counts + 2), total = entries * Hkv;
     const unsigned first = blockIdx.x * kOwnWarps + warp, hop = gridDim.x * kOwnWarps;
 
-    // The copying cursor: unit iu at token itk, the block of that step, and the entry of the unit after.
+    const int bshift = a.g.block_size == 16 ? 4 : 5;
+    // The copying cursor: unit iu (kv head ikvh) at token itk, the block of that step, and the entry of the unit after.
     auto table_at = [&](const OwnItem& it, int tk) {
-        return it.ntok > 0 ? __ldg(a.g.block_tables + (size_t)it.row * a.g.max_blocks_per_seq + tk / a.g.block_size) : 0;
+        return it.ntok > 0 ? __ldg(a.g.block_tables + (size_t)it.row * a.g.max_blocks_per_seq + (tk >> bshift)) : 0;
     };
     unsigned iu = first;
     OwnItem icur = load_own(a.own, iu / Hkv, iu < total ? entries : 0u);
     OwnItem inext = load_own(a.own, (iu + hop) / Hkv, iu + hop < total ? entries : 0u);
-    int itk = icur.tok0, iphys = table_at(icur, itk), ist = 0;
+    int itk = icur.tok0, iphys = table_at(icur, itk), ikvh = (int)(iu % Hkv), ist = 0;
     // lane's chunk of rows lane / CPR, + 32 / CPR, ...: the swizzle repeats every 8 rows
     constexpr int RPI = 32 / CPR;
     const int crow = lane / CPR, cch = lane % CPR;
     auto issue = [&]() {
         if (iu < total) {
-            const int kvh = (int)(iu % Hkv);
             const uint32_t dst = ring + ist * C::STAGE;
             if (icur.ntok > 0) {
                 int phys = iphys;
@@ -477,7 +491,8 @@ __global__ void __launch_bounds__(kOwnThreads, 2) shared_own_kernel(const __grid
                     if (lane == 0) atomicOr(a.g.status, PA_DEV_BAD_BLOCK);
                     phys = 0;
                 }
-                const size_t off = ((((size_t)phys * Hkv + kvh) * a.g.block_size + itk % a.g.block_size) * D) * 2 + lane * 16;
+                const unsigned row = ((unsigned)phys * Hkv + ikvh) * (1u << bshift) + (itk & ((1 << bshift) - 1));  // < 2^31
+                const size_t off = (size_t)row * (D * 2) + lane * 16;
                 const char* kp = static_cast<const char*>(a.g.k_cache) + off;
                 const char* vp = static_cast<const char*>(a.g.v_cache) + off;
 #pragma unroll
@@ -489,7 +504,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2) shared_own_kernel(const __grid
                 }
                 if (itk == icur.tok0) {
                     const char* qp = static_cast<const char*>(a.g.q) +
-                                     ((size_t)icur.row * a.g.num_heads + (size_t)kvh * G) * (D * 2);
+                                     ((size_t)icur.row * a.g.num_heads + (size_t)ikvh * G) * (D * 2);
 #pragma unroll
                     for (int i = 0; i < (G * CPR + 31) / 32; ++i)
                         if (i * 32 + lane < G * CPR)
@@ -501,6 +516,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2) shared_own_kernel(const __grid
                 itk += kStep;
             } else {
                 iu += hop;
+                ikvh = (int)(iu % Hkv);
                 icur = inext;
                 inext = load_own(a.own, (iu + hop) / Hkv, iu + hop < total ? entries : 0u);
                 itk = icur.tok0;
