@@ -622,73 +622,93 @@ __global__ void __launch_bounds__(128) group_merge_kernel(const GroupArgs a)
 // (tokens x tiles x kv heads) over twice the resident CTAs, at least 256 tokens.
 constexpr int kPlanThreads = 1024;
 
-__global__ void __launch_bounds__(kPlanThreads) cross_plan_kernel(const CrossArgs a, int T, int ctas)
+__global__ void __launch_bounds__(kPlanThreads, 1) cross_plan_kernel(const CrossArgs a, int T, int ctas)
 {
     __shared__ unsigned long long s_work;
     __shared__ unsigned s_items, s_merges;
+    __shared__ int s_q0[kPlanThreads], s_n[kPlanThreads], s_len[kPlanThreads];
     pdl_launch_dependents();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cap = min(a.max_context_len, (int)min((long long)a.g.max_blocks_per_seq * a.g.block_size, 0x7fffffffll));
-    if (threadIdx.x == 0) {
+    const bool split = a.max_chunks > 1;
+    if (tid == 0) {
         s_work = 0;
         s_items = s_merges = 0;
     }
-    __syncthreads();
-    unsigned long long work = 0;
-    for (int s = threadIdx.x; s < a.num_seqs; s += kPlanThreads) {
+    // rows and tokens of sequence s; no rows where its data is bad
+    auto load = [&](int s, bool flag) {
         const int q0 = __ldg(a.q_start + s), q1 = __ldg(a.q_start + s + 1), L = __ldg(a.context_lens + s);
-        if (q0 < 0 || q1 > a.num_query_tokens || q1 < q0 || q1 - q0 > a.max_query_len || L < 0 || L > cap)
-            atomicOr(a.g.status, PA_DEV_BAD_CONTEXT);
-        else
-            work += (unsigned long long)((q1 - q0 + T - 1) / T) * L;
+        const bool bad = q0 < 0 || q1 > a.num_query_tokens || q1 < q0 || q1 - q0 > a.max_query_len || L < 0 || L > cap;
+        if (bad && flag) atomicOr(a.g.status, PA_DEV_BAD_CONTEXT);
+        s_q0[tid] = q0;
+        s_n[tid] = bad ? 0 : q1 - q0;
+        s_len[tid] = L;
+        return bad ? 0ull : (unsigned long long)((q1 - q0 + T - 1) / T) * L;
+    };
+    const bool one = a.num_seqs <= kPlanThreads;  // a batch this small is loaded once
+    unsigned long long work = 0;
+    if (split || !one)
+        for (int s = tid; s < a.num_seqs; s += kPlanThreads) work += load(s, true);
+    else if (tid < a.num_seqs)
+        load(tid, true);
+    if (split) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) work += __shfl_xor_sync(0xffffffffu, work, o);
+        __syncthreads();
+        if (lane == 0 && work) atomicAdd(&s_work, work);
     }
-    if (work) atomicAdd(&s_work, work);
     __syncthreads();
-    const unsigned long long share = s_work * a.g.num_kv_heads / (2ull * ctas);
+    const int share = (int)fminf((float)s_work * (float)a.g.num_kv_heads / (2.f * (float)ctas), 1e9f);
     const int least = (a.max_context_len + a.max_chunks - 1) / a.max_chunks;
-    const int chunk = (max(max((int)min(share, 1ull << 30), least), 256) + kTok - 1) / kTok * kTok;
+    const int chunk = (max(max(share, least), 256) + kTok - 1) / kTok * kTok;
     GroupItem* items = const_cast<GroupItem*>(a.g.items);
     uint2* merges = const_cast<uint2*>(a.g.merge_list);
-    for (int s = warp; s < a.num_seqs; s += kPlanThreads / 32) {
-        const int q0 = __ldg(a.q_start + s), q1 = __ldg(a.q_start + s + 1), L = __ldg(a.context_lens + s);
-        const int rows = q1 - q0;
-        if (q0 < 0 || q1 > a.num_query_tokens || rows <= 0 || rows > a.max_query_len || L < 0 || L > cap) continue;
-        const int tiles = (rows + T - 1) / T;
-        const int want = max(1, (L + chunk - 1) / chunk);
-        const int per = max(1, ((L + want - 1) / want + kTok - 1) / kTok) * kTok;
-        const int nch = max(1, (L + per - 1) / per);
-        unsigned i0 = 0, m0 = 0;
-        if (lane == 0) {
-            i0 = atomicAdd(&s_items, (unsigned)(tiles * nch));
-            m0 = nch > 1 ? atomicAdd(&s_merges, (unsigned)rows) : 0u;
+    for (int s0 = 0; s0 < a.num_seqs; s0 += kPlanThreads) {
+        if (!one) {
+            __syncthreads();
+            if (s0 + tid < a.num_seqs) load(s0 + tid, false);
+            __syncthreads();
         }
-        i0 = __shfl_sync(0xffffffffu, i0, 0);
-        m0 = __shfl_sync(0xffffffffu, m0, 0);
-        // rows listed twice (q_start running backwards elsewhere) can ask for more than there is room for
-        if (i0 + tiles * nch > (unsigned)a.g.max_entries || (nch > 1 && m0 + rows > (unsigned)a.g.max_merges)) {
-            if (lane == 0) atomicOr(a.g.status, PA_DEV_BAD_CONTEXT);
-            for (unsigned i = i0 + lane; i < min(i0 + tiles * nch, (unsigned)a.g.max_entries); i += 32)
-                items[i] = GroupItem{0, 0, 0, 0, 0, 0, {0, 0}};
-            for (unsigned i = m0 + lane; nch > 1 && i < min(m0 + rows, (unsigned)a.g.max_merges); i += 32)
-                merges[i] = make_uint2((unsigned)q0, 0u);
-            continue;
+        for (int i = warp; i < min(kPlanThreads, a.num_seqs - s0); i += kPlanThreads / 32) {
+            const int q0 = s_q0[i], rows = s_n[i], L = s_len[i];
+            if (rows == 0) continue;
+            const int tiles = (rows + T - 1) / T;
+            const int want = L <= chunk ? 1 : (L + chunk - 1) / chunk;
+            const int per = max(1, ((L + want - 1) / want + kTok - 1) / kTok) * kTok;
+            const int nch = L <= per ? 1 : (L + per - 1) / per;
+            unsigned i0 = 0, m0 = 0;
+            if (lane == 0) {
+                i0 = atomicAdd(&s_items, (unsigned)(tiles * nch));
+                m0 = nch > 1 ? atomicAdd(&s_merges, (unsigned)rows) : 0u;
+            }
+            i0 = __shfl_sync(0xffffffffu, i0, 0);
+            m0 = __shfl_sync(0xffffffffu, m0, 0);
+            // rows listed twice (q_start running backwards elsewhere) can ask for more than there is room for
+            if (i0 + tiles * nch > (unsigned)a.g.max_entries || (nch > 1 && m0 + rows > (unsigned)a.g.max_merges)) {
+                if (lane == 0) atomicOr(a.g.status, PA_DEV_BAD_CONTEXT);
+                for (unsigned k = i0 + lane; k < min(i0 + tiles * nch, (unsigned)a.g.max_entries); k += 32)
+                    items[k] = GroupItem{0, 0, 0, 0, 0, 0, {0, 0}};
+                for (unsigned k = m0 + lane; nch > 1 && k < min(m0 + rows, (unsigned)a.g.max_merges); k += 32)
+                    merges[k] = make_uint2((unsigned)q0, 0u);
+                continue;
+            }
+            for (int k = lane; k < tiles * nch; k += 32) {
+                const int ch = nch > 1 ? k / tiles : 0, tile = k - ch * tiles;
+                GroupItem it{};
+                it.table_row = s0 + i;
+                it.row0 = q0 + tile * T;
+                it.members = min(T, rows - tile * T);
+                it.chunk = nch > 1 ? ch : -1;
+                it.kv0 = ch * per;
+                it.kvlen = min(per, L - ch * per);
+                items[i0 + k] = it;
+            }
+            if (nch > 1)
+                for (int k = lane; k < rows; k += 32) merges[m0 + k] = make_uint2((unsigned)(q0 + k), (unsigned)nch);
         }
-        for (int i = lane; i < tiles * nch; i += 32) {
-            const int ch = i / tiles, tile = i % tiles;
-            GroupItem it{};
-            it.table_row = s;
-            it.row0 = q0 + tile * T;
-            it.members = min(T, rows - tile * T);
-            it.chunk = nch > 1 ? ch : -1;
-            it.kv0 = ch * per;
-            it.kvlen = min(per, L - ch * per);
-            items[i0 + i] = it;
-        }
-        if (nch > 1)
-            for (int i = lane; i < rows; i += 32) merges[m0 + i] = make_uint2((unsigned)(q0 + i), (unsigned)nch);
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
+    if (tid == 0) {
         unsigned* counts = const_cast<unsigned*>(a.g.counts);
         counts[0] = min(s_items, (unsigned)a.g.max_entries);
         counts[1] = min(s_merges, (unsigned)a.g.max_merges);

@@ -51,70 +51,86 @@ __device__ __forceinline__ OwnItem load_own(const OwnItem* items, unsigned i, un
 __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const SharedArgs a, int T, int group_ctas, int own_warps)
 {
     __shared__ int s_listed[kPlanThreads], s_ctx[kPlanThreads], s_lead[kPlanThreads], s_states[kPlanThreads];
+    __shared__ int s_rows[kPlanThreads], s_start[kPlanThreads + 1], s_len[kPlanThreads], s_ok[kPlanThreads];
     __shared__ unsigned long long s_work, s_own;
     __shared__ unsigned s_items, s_big, s_front, s_back;
     __shared__ int s_bad;
     pdl_launch_dependents();
-    const int B = a.g.block_size, S = a.num_seqs;
+    const int B = a.g.block_size, S = a.num_seqs, NG = a.num_groups, R = a.num_group_rows;
+    const int bshift = B == 16 ? 4 : 5;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const bool small = S <= kPlanThreads;
+    const bool small = S <= kPlanThreads && NG <= kPlanThreads;  // (R <= S)
     volatile int* listed = small ? s_listed : a.listed;
     volatile int* ctx = small ? s_ctx : a.ctx;
     volatile int* lead_blocks = small ? s_lead : a.lead_blocks;
     volatile int* lead_states = small ? s_states : a.lead_states;
+    volatile int* group_ok = small ? s_ok : a.group_ok;
+    const int* rows = small ? s_rows : a.group_rows;
+    const int* start = small ? s_start : a.group_start;
+    const int* lens = small ? s_len : a.shared_lens;
     if (tid == 0) {
         s_work = s_own = 0;
         s_items = s_big = s_front = s_back = 0;
         s_bad = 0;
     }
+    if (small) {
+        // everything the plan reads, in one trip
+        const int r = tid < R ? __ldg(a.group_rows + tid) : 0;
+        const int n = tid < NG ? __ldg(a.shared_lens + tid) : 0;
+        const int g0 = NG > 0 && tid <= NG ? __ldg(a.group_start + tid) : 0;
+        if (tid < R) s_rows[tid] = r;
+        if (tid < NG) s_len[tid] = n;
+        if (tid <= NG) s_start[tid] = g0;
+        if (tid == 0 && NG == kPlanThreads) s_start[NG] = __ldg(a.group_start + NG);
+    }
     const int cap = min(a.max_context_len, (int)min((long long)a.g.max_blocks_per_seq * B, 0x7fffffffll));
     for (int s = tid; s < S; s += kPlanThreads) {
-        listed[s] = 0;
-        lead_blocks[s] = 0;
-        lead_states[s] = 0;
         int L = __ldg(a.context_lens + s);
         if (L < 0 || L > cap) {
             atomicOr(a.g.status, PA_DEV_BAD_CONTEXT);
             L = L < 0 ? 0 : cap;
         }
+        listed[s] = 0;
+        lead_blocks[s] = 0;
+        lead_states[s] = 0;
         ctx[s] = L;
     }
     __syncthreads();
-    for (int g = tid; g < a.num_groups; g += kPlanThreads) {
-        const int r0 = __ldg(a.group_start + g), r1 = __ldg(a.group_start + g + 1);
-        if (r0 < 0 || r1 < r0 || r1 > a.num_group_rows) s_bad = 1;
+    for (int g = tid; g < NG; g += kPlanThreads) {
+        const int r0 = start[g], r1 = start[g + 1];
+        if (r0 < 0 || r1 < r0 || r1 > R) s_bad = 1;
     }
-    for (int i = tid; i < a.num_group_rows; i += kPlanThreads) {
-        const int s = __ldg(a.group_rows + i);
+    for (int i = tid; i < R; i += kPlanThreads) {
+        const int s = rows[i];
         if ((unsigned)s < (unsigned)S) atomicAdd(const_cast<int*>(listed) + s, 1);
     }
     __syncthreads();
     if (tid == 0 && s_bad) atomicOr(a.g.status, PA_DEV_BAD_CONTEXT);
-    const int ngroups = s_bad ? 0 : a.num_groups;
+    const int ngroups = s_bad ? 0 : NG;
     for (int g = warp; g < ngroups; g += kPlanThreads / 32) {
-        const int r0 = __ldg(a.group_start + g), r1 = __ldg(a.group_start + g + 1), n = __ldg(a.shared_lens + g);
-        bool ok = n >= 0 && n <= a.max_shared_len && n % B == 0;
+        const int r0 = start[g], r1 = start[g + 1], n = lens[g];
+        bool ok = n >= 0 && n <= a.max_shared_len && (n & (B - 1)) == 0;
         for (int i = r0 + lane; i < r1; i += 32) {
-            const int s = __ldg(a.group_rows + i);
+            const int s = rows[i];
             ok = ok && (unsigned)s < (unsigned)S;
             ok = ok && listed[s] == 1 && n <= ctx[s];
         }
         ok = __all_sync(0xffffffffu, ok) != 0;
         if (lane == 0) {
-            a.group_ok[g] = ok && n > 0 && r1 > r0;
+            group_ok[g] = ok && n > 0 && r1 > r0;
             if (!ok) atomicOr(a.g.status, PA_DEV_BAD_CONTEXT);
             else if (n > 0) atomicAdd(&s_work, (unsigned long long)((r1 - r0 + T - 1) / T) * n);
         }
     }
     __syncthreads();
     if (s_work > 0) {
-        const unsigned long long share = s_work * a.g.num_kv_heads / (2ull * group_ctas);
+        const int share = (int)fminf((float)s_work * (float)a.g.num_kv_heads / (2.f * (float)group_ctas), 1e9f);
         const int least = (a.max_shared_len + a.max_chunks - 1) / a.max_chunks;
-        const int chunk = (max(max((int)min(share, 1ull << 30), least), 256) + 63) / 64 * 64;
+        const int chunk = (max(max(share, least), 256) + 63) / 64 * 64;
         GroupItem* items = const_cast<GroupItem*>(a.g.items);
         for (int g = warp; g < ngroups; g += kPlanThreads / 32) {
-            if (!*(volatile int*)(a.group_ok + g)) continue;
-            const int r0 = __ldg(a.group_start + g), r1 = __ldg(a.group_start + g + 1), n = __ldg(a.shared_lens + g);
+            if (!group_ok[g]) continue;
+            const int r0 = start[g], r1 = start[g + 1], n = lens[g];
             const int tiles = (r1 - r0 + T - 1) / T;
             const int want = (n + chunk - 1) / chunk;
             const int per = ((n + want - 1) / want + 63) / 64 * 64;
@@ -122,7 +138,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
             unsigned i0 = 0;
             if (lane == 0) i0 = atomicAdd(&s_items, (unsigned)(tiles * nch));
             i0 = __shfl_sync(0xffffffffu, i0, 0);
-            const int first = __ldg(a.group_rows + r0);
+            const int first = rows[r0];
             for (int i = lane; i < tiles * nch; i += 32) {
                 const int ch = i / tiles, tile = i % tiles;
                 GroupItem it{};
@@ -135,8 +151,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
                 items[i0 + i] = it;
             }
             for (int i = r0 + lane; i < r1; i += 32) {
-                const int s = __ldg(a.group_rows + i);
-                lead_blocks[s] = n / B;
+                const int s = rows[i];
+                lead_blocks[s] = n >> bshift;
                 lead_states[s] = nch;
             }
         }
@@ -148,28 +164,29 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
     for (int o = 16; o > 0; o >>= 1) tok += __shfl_xor_sync(0xffffffffu, tok, o);
     if (lane == 0 && tok) atomicAdd(&s_own, tok);
     __syncthreads();
-    const int share = (int)min(s_own * a.g.num_kv_heads / (2ull * own_warps), 1ull << 30);
+    const int share = (int)fminf((float)s_own * (float)a.g.num_kv_heads / (2.f * (float)own_warps), 1e9f);
     // tokens of a row's parts, all the same but the last
     auto part_of = [&](int own) {
-        const int least = (own + a.max_parts - 1) / a.max_parts;
-        const int p = (max(max(share, least), 256) + 15) / 16 * 16;
+        const int p0 = max(share, 256);
+        if (own <= p0) return max(own, 1);
+        const int p = (max(p0, (own + a.max_parts - 1) / a.max_parts) + 15) / 16 * 16;
         const int n = (own + p - 1) / p;
-        return n <= 1 ? max(own, 1) : ((own + n - 1) / n + 15) / 16 * 16;
+        return n <= 1 ? own : ((own + n - 1) / n + 15) / 16 * 16;
     };
     const int big = max(32, share / 2);  // an entry of the first half
     unsigned nbig = 0;
     for (int s = tid; s < S; s += kPlanThreads) {
         const int own = ctx[s] - lead_blocks[s] * B, per = part_of(own);
-        nbig += per > big ? (unsigned)((own + per - 1) / per) : 0u;
+        nbig += per > big ? (own <= per ? 1u : (unsigned)((own + per - 1) / per)) : 0u;
     }
     if (nbig) atomicAdd(&s_big, nbig);
     __syncthreads();
     for (int s = tid; s < S; s += kPlanThreads) {
         const int tok0 = lead_blocks[s] * B, own = ctx[s] - tok0, lead = lead_states[s];
-        const int per = part_of(own), parts = max(1, (own + per - 1) / per);
+        const int per = part_of(own), parts = own <= per ? 1 : (own + per - 1) / per;
         const unsigned i0 = per > big ? atomicAdd(&s_front, (unsigned)parts) : s_big + atomicAdd(&s_back, (unsigned)parts);
         for (int p = 0; p < parts; ++p)
-            a.own[i0 + p] = OwnItem{s, tok0 + p * per, max(0, min(per, own - p * per)), lead, p, parts, {0, 0}};
+            a.own[i0 + p] = OwnItem{s, tok0 + p * per, min(per, own - p * per), lead, p, parts, {0, 0}};
         if (parts > 1)
             for (int h = 0; h < a.g.num_kv_heads; ++h) a.arrived[(size_t)s * a.g.num_kv_heads + h] = 0u;
     }
