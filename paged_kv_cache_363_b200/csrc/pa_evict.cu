@@ -10,9 +10,13 @@
 // < n) are disjoint, so the moves run in any order.
 //
 // Two kernels.  evict_select (one CTA per (sequence, kv head)) finds the n-th largest key by
-// radix selection, 8 bits a pass, marks the kept tokens in a bit mask in shared memory, ranks
+// radix selection, 11 bits a pass, marks the kept tokens in a bit mask in shared memory, ranks
 // gaps and movers by prefix sums over the mask's words, and writes the move list and the new
 // scores and positions.  evict_move copies the K and V rows of the list.
+// The selection is a chain of passes over the head's tokens, each a trip to memory long, and
+// there may be fewer heads than SMs: scores and positions are read once, eight loads in flight
+// per thread, and the keys stay in shared memory (contexts up to kCachedContext; longer ones
+// read them again in every pass).
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -24,23 +28,26 @@
 namespace pa {
 namespace {
 
-constexpr int kSelThreads = 1024;
 constexpr int kMoveThreads = 256;
+constexpr int kBins = 2048;
+constexpr int kCachedContext = 49152;  // keys (4 bytes) and two masks of a context in shared memory
 
-// Scores in an unsigned order: larger is better, -0 and +0 alike, NaN above +inf, and every
-// recent token above all of them.
-__device__ __forceinline__ uint32_t rank_key(float score, int pos, int first_recent)
+// Scores in an unsigned order: larger is better, -0 and +0 alike, NaN above +inf.  Recent tokens
+// (the key's largest value) come above all of them.
+__device__ __forceinline__ uint32_t score_key(float score)
 {
-    if (pos >= first_recent) return 0xffffffffu;
     if (score != score) return 0xfffffffeu;
     const uint32_t b = __float_as_uint(score + 0.f);
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
+constexpr uint32_t kRecentKey = 0xffffffffu;
 
 // Exclusive prefix sum of one value per thread over the CTA; *total receives the sum.
+template <int THREADS>
 __device__ __forceinline__ unsigned long long block_scan(unsigned long long v, unsigned long long* s_warp,
                                                          unsigned long long* total)
 {
+    constexpr int NW = THREADS / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     unsigned long long x = v;
 #pragma unroll
@@ -50,29 +57,29 @@ __device__ __forceinline__ unsigned long long block_scan(unsigned long long v, u
     }
     if (lane == 31) s_warp[warp] = x;
     __syncthreads();
-    if (warp == 0) {
-        unsigned long long w = s_warp[lane];
+    unsigned long long w = lane < NW ? s_warp[lane] : 0ull;  // every warp adds up the warps' sums itself
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const unsigned long long y = __shfl_up_sync(0xffffffffu, w, o);
-            if (lane >= o) w += y;
-        }
-        s_warp[lane] = w;
+    for (int o = 1; o < NW; o <<= 1) {
+        const unsigned long long y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += y;
     }
+    *total = __shfl_sync(0xffffffffu, w, NW - 1);
+    const unsigned long long base = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
     __syncthreads();
-    *total = s_warp[kSelThreads / 32 - 1];
-    const unsigned long long base = warp ? s_warp[warp - 1] : 0ull;
-    __syncthreads();
-    return base + x - v;
+    return (warp > 0 ? base : 0ull) + x - v;
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a)
+// CACHED: the keys stay in shared memory behind the masks.
+template <int THREADS, bool CACHED>
+__global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictArgs a)
 {
-    extern __shared__ uint32_t s_mask[];  // kept tokens, then (second half) the ties: one bit each
-    __shared__ unsigned s_hist[256];
-    __shared__ unsigned long long s_warp[kSelThreads / 32];
+    constexpr int UN = 8;                        // loads in flight per thread
+    constexpr int BPT = kBins / THREADS;         // bins per thread
+    extern __shared__ uint32_t s_mask[];         // kept tokens, then the ties: one bit each; then the keys
+    __shared__ unsigned s_hist[kBins];
+    __shared__ unsigned long long s_warp[THREADS / 32];
     __shared__ unsigned s_prefix, s_need;
-    __shared__ int s_max[kSelThreads / 32];
+    __shared__ int s_max[THREADS / 32];
     const int sh = blockIdx.x;
     const int s = sh / a.num_kv_heads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -92,72 +99,98 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     float* nsc = a.new_scores + row;
     int* npos = a.new_positions + row;
     if (n == L || n == 0) {
-        for (int i = tid; i < n; i += kSelThreads) {
+        for (int i = tid; i < n; i += THREADS) {
             nsc[i] = sc[i];
             npos[i] = pos[i];
         }
         if (tid == 0) a.counts[sh] = 0;
         return;
     }
-    // the recent tokens: positions within num_recent of the largest
+    const int words = (L + 31) / 32;
+    uint32_t* s_tie = s_mask + words;
+    uint32_t* s_key = s_tie + words;
+    // keys, and the largest position
     int mx = INT32_MIN;
-    for (int i = tid; i < L; i += kSelThreads) mx = max(mx, pos[i]);
+    for (int i0 = tid; i0 < L; i0 += THREADS * UN) {
+        float x[UN];
+        int p[UN];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        for (int k = 0; k < UN; ++k) {
+            const int i = i0 + k * THREADS;
+            p[k] = i < L ? pos[i] : INT32_MIN;
+            if constexpr (CACHED) x[k] = i < L ? sc[i] : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < UN; ++k) {
+            mx = max(mx, p[k]);
+            if constexpr (CACHED)
+                if (i0 + k * THREADS < L) s_key[i0 + k * THREADS] = score_key(x[k]);
+        }
+    }
+    mx = __reduce_max_sync(0xffffffffu, mx);
     if (lane == 0) s_max[warp] = mx;
+    for (int i = tid; i < kBins; i += THREADS) s_hist[i] = 0;
     __syncthreads();
-    mx = s_max[lane];
+    mx = __reduce_max_sync(0xffffffffu, lane < THREADS / 32 ? s_max[lane] : INT32_MIN);
+    // the recent tokens: positions within num_recent of the largest
+    const int recent = min(a.num_recent, n);
+    const long long fr = (long long)mx - recent + 1;
+    const int first_recent = fr < (long long)INT32_MIN ? INT32_MIN : (int)min(fr, (long long)INT32_MAX);
+    if constexpr (CACHED) {
+        if (recent > 0) {
+            for (int i0 = tid; i0 < L; i0 += THREADS * UN) {
+                int p[UN];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    const long long fr = (long long)mx - min(a.num_recent, n) + 1;
-    const int first_recent = fr < (long long)INT32_MIN ? INT32_MIN : (int)fr;  // mx + 1 (none recent) needs fr > mx
-    const bool none_recent = min(a.num_recent, n) == 0;
-    auto key = [&](int i) {
-        return none_recent ? rank_key(sc[i], -1, 0) : rank_key(sc[i], pos[i], first_recent);
+                for (int k = 0; k < UN; ++k) p[k] = i0 + k * THREADS < L ? pos[i0 + k * THREADS] : INT32_MIN;
+#pragma unroll
+                for (int k = 0; k < UN; ++k)
+                    if (i0 + k * THREADS < L && p[k] >= first_recent) s_key[i0 + k * THREADS] = kRecentKey;
+            }
+        }
+        // (a thread reads back the keys it wrote itself until the masks below)
+    }
+    auto key = [&](int i) -> uint32_t {
+        if constexpr (CACHED) return s_key[i];
+        return recent > 0 && pos[i] >= first_recent ? kRecentKey : score_key(sc[i]);
     };
-    // radix selection of the n-th largest key
+    // radix selection of the n-th largest key: bits 31-21, 20-10, 9-0
     unsigned prefix = 0, need = (unsigned)n;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) s_hist[tid] = 0;
-        __syncthreads();
-        const unsigned hi_mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-        for (int i = tid; i < L; i += kSelThreads) {
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+        const unsigned hi_mask = pass == 0 ? 0u : 0xffffffffu << (shift + (pass == 1 ? 11 : 10));
+        const unsigned bin_mask = pass == 2 ? 1023u : 2047u;
+        for (int i = tid; i < L; i += THREADS) {
             const uint32_t k = key(i);
-            if ((k & hi_mask) == prefix) atomicAdd(&s_hist[(k >> shift) & 255u], 1u);
+            if ((k & hi_mask) == prefix) atomicAdd(&s_hist[(k >> shift) & bin_mask], 1u);
         }
         __syncthreads();
-        if (warp == 0) {
-            // lane l holds bins 255 - 8l .. 248 - 8l, from the top
-            unsigned c[8], sum = 0;
+        // thread t holds bins kBins - 1 - BPT * t and down
+        unsigned c[BPT], sum = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum += c[j] = s_hist[255 - 8 * lane - j];
-            unsigned x = sum;
+        for (int j = 0; j < BPT; ++j) {
+            const int bin = kBins - 1 - BPT * tid - j;
+            sum += c[j] = s_hist[bin];
+            s_hist[bin] = 0;  // for the next pass
+        }
+        unsigned long long total;
+        unsigned above = (unsigned)block_scan<THREADS>(sum, s_warp, &total);
+        if (above < need && need <= above + sum) {
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const unsigned y = __shfl_up_sync(0xffffffffu, x, o);
-                if (lane >= o) x += y;
-            }
-            unsigned above = x - sum;
-            if (above < need && need <= x) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (above < need && need <= above + c[j]) {
-                        s_prefix = prefix | ((unsigned)(255 - 8 * lane - j) << shift);
-                        s_need = need - above;
-                    }
-                    above += c[j];
+            for (int j = 0; j < BPT; ++j) {
+                if (above < need && need <= above + c[j]) {
+                    s_prefix = prefix | ((unsigned)(kBins - 1 - BPT * tid - j) << shift);
+                    s_need = need - above;
+                    need = 0;  // found
                 }
+                above += c[j];
             }
         }
         __syncthreads();
         prefix = s_prefix;
         need = s_need;
-        __syncthreads();
     }
     // masks of the keys above the threshold, and of those equal to it
-    const int words = (L + 31) / 32;
-    uint32_t* s_tie = s_mask + words;
-    for (int w = warp; w < words; w += kSelThreads / 32) {
+    for (int w = warp; w < words; w += THREADS / 32) {
         const int i = w * 32 + lane;
         const uint32_t k = i < L ? key(i) : 0u;
         const uint32_t gt = __ballot_sync(0xffffffffu, i < L && k > prefix);
@@ -169,11 +202,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     }
     __syncthreads();
     // the first `need` ties stay: every thread ranks a run of words
-    const int per = (words + kSelThreads - 1) / kSelThreads;
+    const int per = (words + THREADS - 1) / THREADS;
     const int w0 = min(words, tid * per), w1 = min(words, w0 + per);
     unsigned long long cnt = 0, total;
     for (int w = w0; w < w1; ++w) cnt += __popc(s_tie[w]);
-    unsigned long long rank = block_scan(cnt, s_warp, &total);
+    unsigned long long rank = block_scan<THREADS>(cnt, s_warp, &total);
     cnt = 0;
     for (int w = w0; w < w1; ++w) {
         uint32_t t = s_tie[w], take = 0;
@@ -189,7 +222,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
         cnt += (unsigned long long)__popc(~kept & front) | (unsigned long long)__popc(kept & ~front) << 32;
     }
     // gaps before slot n (low half) and kept tokens behind it (high half): as many of each
-    rank = block_scan(cnt, s_warp, &total);
+    rank = block_scan<THREADS>(cnt, s_warp, &total);
     uint2* moves = a.moves + (size_t)sh * a.move_stride;
     unsigned gap = (unsigned)rank, mover = (unsigned)(rank >> 32);
     for (int w = w0; w < w1; ++w) {
@@ -203,15 +236,45 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     __syncthreads();
     // the scores and positions of the slots before n (these arrays may be the old ones: a slot
     // before n is only ever written with its own value or one from behind n)
-    for (int i = tid; i < n; i += kSelThreads)
-        if (s_mask[i / 32] >> (i % 32) & 1u) {
-            nsc[i] = sc[i];
-            npos[i] = pos[i];
+    for (int i0 = tid; i0 < n; i0 += THREADS * UN) {
+        float x[UN];
+        int p[UN];
+#pragma unroll
+        for (int k = 0; k < UN; ++k) {
+            const int i = i0 + k * THREADS;
+            if (i < n) {
+                x[k] = sc[i];
+                p[k] = pos[i];
+            }
         }
-    for (unsigned r = tid; r < (unsigned)total; r += kSelThreads) {
-        const uint2 m = moves[r];
-        nsc[m.x] = sc[m.y];
-        npos[m.x] = pos[m.y];
+#pragma unroll
+        for (int k = 0; k < UN; ++k) {
+            const int i = i0 + k * THREADS;
+            if (i < n && (s_mask[i / 32] >> (i % 32) & 1u)) {
+                nsc[i] = x[k];
+                npos[i] = p[k];
+            }
+        }
+    }
+    for (unsigned r0 = tid; r0 < (unsigned)total; r0 += THREADS * 4) {
+        uint2 m[4];
+        float x[4];
+        int p[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (r0 + k * THREADS < (unsigned)total) m[k] = moves[r0 + k * THREADS];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (r0 + k * THREADS < (unsigned)total) {
+                x[k] = sc[m[k].y];
+                p[k] = pos[m[k].y];
+            }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (r0 + k * THREADS < (unsigned)total) {
+                nsc[m[k].x] = x[k];
+                npos[m[k].x] = p[k];
+            }
     }
 }
 
@@ -255,13 +318,16 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
 cudaError_t launch_evict(const EvictArgs& a, int head_dim, int elt_bytes, cudaStream_t stream)
 {
     const int rows = a.num_seqs * a.num_kv_heads;
-    const size_t smem = (size_t)((a.max_context_len + 31) / 32) * 8;
+    const int words = (a.max_context_len + 31) / 32;
+    // 256 threads have eight tokens each of a context of 2048, and cheaper barriers (a budget of 1024
+    // tokens: MEASURE); the longest contexts want all the loads an SM can have in flight
+    const bool cached = a.max_context_len <= kCachedContext, few = a.max_context_len <= 4096;
+    const size_t smem = (size_t)words * 8 + (cached ? (size_t)a.max_context_len * 4 : 0);
+    auto kernel = few ? evict_select_kernel<256, true>
+                      : (cached ? evict_select_kernel<1024, true> : evict_select_kernel<1024, false>);
     cudaError_t e;
-    if (smem > 40 * 1024) {
-        e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
-    evict_select_kernel<<<rows, kSelThreads, smem, stream>>>(a);
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
+    kernel<<<rows, few ? 256 : 1024, smem, stream>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     // enough CTAs to fill the device, but none with less than one step of the longest list
     const int cpr = head_dim * elt_bytes / 16;
