@@ -31,6 +31,12 @@ namespace {
 constexpr int kMoveThreads = 256;
 constexpr int kBins = 2048;
 constexpr int kCachedContext = 49152;  // keys (4 bytes) and two masks of a context in shared memory
+constexpr int kSmallContext = 4096;    // scores, positions, blocks and the move list as well
+
+// Where the head's tokens are kept while they are selected.
+constexpr int kFromGlobal = 0;  // nowhere: read again in every pass
+constexpr int kKeysCached = 1;  // their keys in shared memory
+constexpr int kAllCached = 2;   // scores, positions and the move list too; the CTA may move the rows itself
 
 // Scores in an unsigned order: larger is better, -0 and +0 alike, NaN above +inf.  Recent tokens
 // (the key's largest value) come above all of them.
@@ -69,13 +75,14 @@ __device__ __forceinline__ unsigned long long block_scan(unsigned long long v, u
     return (warp > 0 ? base : 0ull) + x - v;
 }
 
-// CACHED: the keys stay in shared memory behind the masks.
-template <int THREADS, bool CACHED>
+// CPR: with kAllCached, 16-byte chunks of a K or V row when this kernel moves the rows too, else 0.
+template <int THREADS, int WHERE, int CPR>
 __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictArgs a)
 {
+    constexpr bool CACHED = WHERE != kFromGlobal, ALL = WHERE == kAllCached, MOVE = CPR > 0;
     constexpr int UN = 8;                        // loads in flight per thread
     constexpr int BPT = kBins / THREADS;         // bins per thread
-    extern __shared__ uint32_t s_mask[];         // kept tokens, then the ties: one bit each; then the keys
+    extern __shared__ uint32_t s_mask[];         // kept tokens, then the ties: one bit each; then what is cached
     __shared__ unsigned s_hist[kBins];
     __shared__ unsigned long long s_warp[THREADS / 32];
     __shared__ unsigned s_prefix, s_need;
@@ -84,10 +91,10 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictArgs a
     const int s = sh / a.num_kv_heads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int L = __ldg(a.context_lens + s), n = __ldg(a.keep_lens + s);
-    pdl_launch_dependents();
+    if constexpr (!MOVE) pdl_launch_dependents();
     if (L < 0 || n < 0 || L > a.max_context_len || L > a.max_blocks_per_seq * a.block_size) {
         if (tid == 0) {
-            a.counts[sh] = 0;
+            if constexpr (!MOVE) a.counts[sh] = 0;
             if (sh % a.num_kv_heads == 0) atomicOr(a.status, PA_DEV_BAD_CONTEXT);
         }
         return;
@@ -103,12 +110,21 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictArgs a
             nsc[i] = sc[i];
             npos[i] = pos[i];
         }
-        if (tid == 0) a.counts[sh] = 0;
+        if constexpr (!MOVE)
+            if (tid == 0) a.counts[sh] = 0;
         return;
     }
     const int words = (L + 31) / 32;
     uint32_t* s_tie = s_mask + words;
     uint32_t* s_key = s_tie + words;
+    float* s_sc = reinterpret_cast<float*>(s_key + L);
+    int* s_pos = reinterpret_cast<int*>(s_sc + L);
+    int* s_blk = s_pos + L;                                       // the table's row, where rows are moved here
+    const int nblk = MOVE ? (L + a.block_size - 1) / a.block_size : 0;
+    uint16_t* s_gap = reinterpret_cast<uint16_t*>(s_blk + nblk);  // [L / 2]
+    uint16_t* s_mover = s_gap + L / 2;                            // [L / 2]
+    if constexpr (MOVE)
+        for (int i = tid; i < nblk; i += THREADS) s_blk[i] = __ldg(a.block_tables + (size_t)s * a.max_blocks_per_seq + i);
     // keys, and the largest position
     int mx = INT32_MIN;
     for (int i0 = tid; i0 < L; i0 += THREADS * UN) {
@@ -123,8 +139,14 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictArgs a
 #pragma unroll
         for (int k = 0; k < UN; ++k) {
             mx = max(mx, p[k]);
+            const int i = i0 + k * THREADS;
             if constexpr (CACHED)
-                if (i0 + k * THREADS < L) s_key[i0 + k * THREADS] = score_key(x[k]);
+                if (i < L) s_key[i] = score_key(x[k]);
+            if constexpr (ALL)
+                if (i < L) {
+                    s_sc[i] = x[k];
+                    s_pos[i] = p[k];
+                }
         }
     }
     mx = __reduce_max_sync(0xffffffffu, mx);
@@ -141,7 +163,8 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictArgs a
             for (int i0 = tid; i0 < L; i0 += THREADS * UN) {
                 int p[UN];
 #pragma unroll
-                for (int k = 0; k < UN; ++k) p[k] = i0 + k * THREADS < L ? pos[i0 + k * THREADS] : INT32_MIN;
+                for (int k = 0; k < UN; ++k)
+                    p[k] = i0 + k * THREADS < L ? (ALL ? s_pos[i0 + k * THREADS] : pos[i0 + k * THREADS]) : INT32_MIN;
 #pragma unroll
                 for (int k = 0; k < UN; ++k)
                     if (i0 + k * THREADS < L && p[k] >= first_recent) s_key[i0 + k * THREADS] = kRecentKey;
@@ -229,11 +252,59 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictArgs a
         const uint32_t kept = s_mask[w];
         const int below = n - w * 32;
         const uint32_t front = below >= 32 ? 0xffffffffu : (below <= 0 ? 0u : (1u << below) - 1u);
-        for (uint32_t b = ~kept & front; b; b &= b - 1) moves[gap++].x = (unsigned)(w * 32 + __ffs(b) - 1);
-        for (uint32_t b = kept & ~front; b; b &= b - 1) moves[mover++].y = (unsigned)(w * 32 + __ffs(b) - 1);
+        for (uint32_t b = ~kept & front; b; b &= b - 1) {
+            const int i = w * 32 + __ffs(b) - 1;
+            if constexpr (ALL) s_gap[gap] = (uint16_t)i;
+            if constexpr (!MOVE) moves[gap].x = (unsigned)i;
+            ++gap;
+        }
+        for (uint32_t b = kept & ~front; b; b &= b - 1) {
+            const int i = w * 32 + __ffs(b) - 1;
+            if constexpr (ALL) s_mover[mover] = (uint16_t)i;
+            if constexpr (!MOVE) moves[mover].y = (unsigned)i;
+            ++mover;
+        }
     }
-    if (tid == 0) a.counts[sh] = (unsigned)total;
+    const unsigned count = (unsigned)total;
+    if constexpr (!MOVE)
+        if (tid == 0) a.counts[sh] = count;
     __syncthreads();
+    if constexpr (MOVE) {
+        // the rows first: they are what takes the time
+        constexpr int RPI = THREADS / CPR, MU = 4;  // rows of a step, steps in flight
+        const int kvh = sh % a.num_kv_heads, c = tid % CPR;
+        uint4* kc = static_cast<uint4*>(a.k_cache);
+        uint4* vc = static_cast<uint4*>(a.v_cache);
+        const int bshift = a.block_size == 16 ? 4 : 5;
+        for (unsigned r0 = tid / CPR; r0 < count; r0 += RPI * MU) {
+            uint4 kv[MU], vv[MU];
+            size_t dst[MU];
+            bool ok[MU];
+#pragma unroll
+            for (int k = 0; k < MU; ++k) {
+                const unsigned r = r0 + k * RPI;
+                ok[k] = r < count;
+                if (!ok[k]) continue;
+                const int f = s_mover[r], d = s_gap[r];
+                const int fb = s_blk[f >> bshift], db = s_blk[d >> bshift];
+                if ((unsigned)fb >= (unsigned)a.num_blocks || (unsigned)db >= (unsigned)a.num_blocks) {
+                    if (c == 0) atomicOr(a.status, PA_DEV_BAD_BLOCK);
+                    ok[k] = false;
+                    continue;
+                }
+                const size_t src = ((((size_t)fb * a.num_kv_heads + kvh) << bshift) + (f & (a.block_size - 1))) * CPR + c;
+                dst[k] = ((((size_t)db * a.num_kv_heads + kvh) << bshift) + (d & (a.block_size - 1))) * CPR + c;
+                kv[k] = kc[src];
+                vv[k] = vc[src];
+            }
+#pragma unroll
+            for (int k = 0; k < MU; ++k)
+                if (ok[k]) {
+                    kc[dst[k]] = kv[k];
+                    vc[dst[k]] = vv[k];
+                }
+        }
+    }
     // the scores and positions of the slots before n (these arrays may be the old ones: a slot
     // before n is only ever written with its own value or one from behind n)
     for (int i0 = tid; i0 < n; i0 += THREADS * UN) {
@@ -243,8 +314,8 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictArgs a
         for (int k = 0; k < UN; ++k) {
             const int i = i0 + k * THREADS;
             if (i < n) {
-                x[k] = sc[i];
-                p[k] = pos[i];
+                x[k] = ALL ? s_sc[i] : sc[i];
+                p[k] = ALL ? s_pos[i] : pos[i];
             }
         }
 #pragma unroll
@@ -256,25 +327,33 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictArgs a
             }
         }
     }
-    for (unsigned r0 = tid; r0 < (unsigned)total; r0 += THREADS * 4) {
-        uint2 m[4];
-        float x[4];
-        int p[4];
+    if constexpr (ALL) {
+        for (unsigned r = tid; r < count; r += THREADS) {
+            const int f = s_mover[r], d = s_gap[r];
+            nsc[d] = s_sc[f];
+            npos[d] = s_pos[f];
+        }
+    } else {
+        for (unsigned r0 = tid; r0 < count; r0 += THREADS * 4) {
+            uint2 m[4];
+            float x[4];
+            int p[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (r0 + k * THREADS < (unsigned)total) m[k] = moves[r0 + k * THREADS];
+            for (int k = 0; k < 4; ++k)
+                if (r0 + k * THREADS < count) m[k] = moves[r0 + k * THREADS];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (r0 + k * THREADS < (unsigned)total) {
-                x[k] = sc[m[k].y];
-                p[k] = pos[m[k].y];
-            }
+            for (int k = 0; k < 4; ++k)
+                if (r0 + k * THREADS < count) {
+                    x[k] = sc[m[k].y];
+                    p[k] = pos[m[k].y];
+                }
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (r0 + k * THREADS < (unsigned)total) {
-                nsc[m[k].x] = x[k];
-                npos[m[k].x] = p[k];
-            }
+            for (int k = 0; k < 4; ++k)
+                if (r0 + k * THREADS < count) {
+                    nsc[m[k].x] = x[k];
+                    npos[m[k].x] = p[k];
+                }
+        }
     }
 }
 
@@ -319,18 +398,31 @@ cudaError_t launch_evict(const EvictArgs& a, int head_dim, int elt_bytes, cudaSt
 {
     const int rows = a.num_seqs * a.num_kv_heads;
     const int words = (a.max_context_len + 31) / 32;
-    // 256 threads have eight tokens each of a context of 2048, and cheaper barriers (a budget of 1024
-    // tokens: MEASURE); the longest contexts want all the loads an SM can have in flight
-    const bool cached = a.max_context_len <= kCachedContext, few = a.max_context_len <= 4096;
-    const size_t smem = (size_t)words * 8 + (cached ? (size_t)a.max_context_len * 4 : 0);
-    auto kernel = few ? evict_select_kernel<256, true>
-                      : (cached ? evict_select_kernel<1024, true> : evict_select_kernel<1024, false>);
+    const int cpr = head_dim * elt_bytes / 16;
+    int dev = 0, sms = 148;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    // Contexts of up to 4096 tokens take 256 threads (cheaper barriers) and keep all they need in shared
+    // memory.  With a CTA per SM or more they also move their rows, which saves the second kernel's
+    // launch and the list's way through memory; fewer CTAs would leave the moving to too few SMs.
+    const bool small = a.max_context_len <= kSmallContext, fused = small && rows >= sms;
+    const bool cached = a.max_context_len <= kCachedContext;
+    size_t smem = (size_t)words * 8 + (cached ? (size_t)a.max_context_len * 4 : 0);
+    if (small) smem += (size_t)a.max_context_len * 8 + (size_t)(a.max_context_len / 2) * 4 + (size_t)(a.max_context_len / 16 + 1) * 4;
+    auto kernel = cached ? evict_select_kernel<1024, kKeysCached, 0> : evict_select_kernel<1024, kFromGlobal, 0>;
+    if (small) kernel = evict_select_kernel<256, kAllCached, 0>;
+    if (fused) {
+        switch (cpr) {
+            case 8: kernel = evict_select_kernel<256, kAllCached, 8>; break;
+            case 16: kernel = evict_select_kernel<256, kAllCached, 16>; break;
+            case 32: kernel = evict_select_kernel<256, kAllCached, 32>; break;
+            default: return cudaErrorInvalidValue;
+        }
+    }
     cudaError_t e;
     if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
-    kernel<<<rows, few ? 256 : 1024, smem, stream>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    kernel<<<rows, small ? 256 : 1024, smem, stream>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess || fused) return e;
     // enough CTAs to fill the device, but none with less than one step of the longest list
-    const int cpr = head_dim * elt_bytes / 16;
     const int steps = (a.move_stride + kMoveThreads / cpr - 1) / (kMoveThreads / cpr);
     int splits = (148 * 16 + rows - 1) / rows;
     splits = splits < steps ? splits : steps;

@@ -174,6 +174,52 @@ def test_evict_bit_exact(pa, dt, Hkv, D, B, kind, recent, alias):
     assert np.array_equal(bits(k), bits(want_k)) and np.array_equal(bits(v), bits(want_v))
 
 
+@pytest.mark.parametrize("dt,Hkv,D,B,recent", [("bf16", 8, 128, 16, 16), ("bf16", 8, 64, 32, 0), ("f32", 8, 128, 32, 33),
+                                                ("f32", 16, 64, 16, 7)])
+def test_evict_many_heads(pa, dt, Hkv, D, B, recent):
+    """A kv head per SM and more: the rows are moved by the kernel that selects them."""
+    tdt = {"bf16": torch.bfloat16, "f32": torch.float32}[dt]
+    rng = np.random.default_rng(D + B)
+    lens = [1, 0, 4000, 33, 700] + rng.integers(1, 300, 18).tolist()
+    keep = [1, 3, 100, 32, 699] + [int(rng.integers(0, L + 2)) for L in lens[5:]]
+    p, sc, pos, kp = _evict_case(lens, keep, Hkv, B, D, tdt, seed=D + Hkv, kind="odd")
+    assert len(lens) * Hkv >= 148
+    for alias in (False, True):
+        k, v, nsc, npos = _run_evict(pa, p, sc, pos, kp, recent, alias)
+        assert pa.pa_device_status() == 0
+        want_k, want_v = p.k.clone(), p.v.clone()
+        for s, L in enumerate(lens):
+            n = min(keep[s], L)
+            for h in range(Hkv):
+                src = _evict_ref(sc[s, h, :L].astype(np.float64), pos[s, h, :L], n, recent)
+                assert np.array_equal(nsc[s, h, :n], sc[s, h, src], equal_nan=True), (s, h)
+                assert np.array_equal(npos[s, h, :n], pos[s, h, src]), (s, h)
+                i = np.arange(n)
+                d, f = (p.tables[s][i // B], i % B), (p.tables[s][src // B], src % B)
+                want_k[d[0], h, d[1]] = p.k[f[0], h, f[1]]
+                want_v[d[0], h, d[1]] = p.v[f[0], h, f[1]]
+        assert np.array_equal(bits(k), bits(want_k)) and np.array_equal(bits(v), bits(want_v))
+
+
+def test_evict_bad_blocks_with_many_heads(pa):
+    p, sc, pos, kp = _evict_case([100] * 24, [50] * 24, 8, 16, 64, torch.float32, seed=6)
+    p.tables[3, :] = 10 ** 6
+    p.tables[5, 6] = -1                                     # a block that only movers may lie in
+    k, v, nsc, npos = _run_evict(pa, p, sc, pos, kp, 4, False)
+    assert pa.pa_device_status() == pa.PA_DEV_BAD_BLOCK
+    src = _evict_ref(sc[0, 0, :100].astype(np.float64), pos[0, 0, :100], 50, 4)
+    i = np.arange(50)
+    assert np.array_equal(bits(k[p.tables[0][i // 16], 0, i % 16]), bits(p.k[p.tables[0][src // 16], 0, src % 16]))
+
+
+def test_evict_context_past_what_shared_memory_holds(pa):
+    p, sc, pos, kp = _evict_case([60001, 9], [30000, 4], 1, 32, 64, torch.bfloat16, seed=19, kind="odd")
+    k, v, nsc, npos = _run_evict(pa, p, sc, pos, kp, 77, False)
+    assert pa.pa_device_status() == 0
+    src = _evict_ref(sc[0, 0, :60001].astype(np.float64), pos[0, 0, :60001], 30000, 77)
+    assert np.array_equal(npos[0, 0, :30000], pos[0, 0, src])
+
+
 def test_evict_long_context(pa):
     lens, keep = [40000, 20001], [1000, 19000]
     p, sc, pos, kp = _evict_case(lens, keep, 1, 32, 64, torch.bfloat16, seed=9)
