@@ -761,6 +761,11 @@ cudaError_t launch_group_d(const GroupArgs& a, int group, int tile_rows, int cta
 
 int group_resident_ctas(int sms) { return 2 * sms; }
 
+static bool cross_many_rows(int64_t rows, int64_t max_rows, int group, int num_kv_heads, int sms)
+{
+    return max_rows * group >= 256 && rows * group / 256 * num_kv_heads >= sms;
+}
+
 cudaError_t launch_group(const GroupArgs& a, int head_dim, int group, int tile_rows, int ctas, cudaStream_t stream)
 {
     return head_dim == 64 ? launch_group_d<64>(a, group, tile_rows, ctas, stream)
@@ -777,7 +782,33 @@ cudaError_t launch_group_merge(const GroupArgs& a, int head_dim, cudaStream_t st
 
 cudaError_t launch_cross(const CrossArgs& a, int head_dim, int group, cudaStream_t stream)
 {
-    const int ctas = group_resident_ctas(sm_count());
+    const int sms = sm_count(), ctas = group_resident_ctas(sms);
+    // Many rows: two query tiles of 128 rows per CTA share every K/V tile (pa_prefill.cu), where there are
+    // enough of them to give every SM one whatever the sequences' tokens.  CROSSOVER
+    if (head_dim == 128 && cross_many_rows(a.num_query_tokens, a.max_query_len, group, a.g.num_kv_heads, sms)) {
+        PrefillArgs p{};
+        p.out = a.g.out;
+        p.q = a.g.q;
+        p.k_cache = a.g.k_cache;
+        p.v_cache = a.g.v_cache;
+        p.block_tables = a.g.block_tables;
+        p.context_lens = a.context_lens;
+        p.q_start = a.q_start;
+        p.status = a.g.status;
+        p.sched = const_cast<unsigned*>(a.g.counts);
+        p.num_seqs = a.num_seqs;
+        p.num_heads = a.g.num_heads;
+        p.num_kv_heads = a.g.num_kv_heads;
+        p.max_blocks_per_seq = a.g.max_blocks_per_seq;
+        p.num_blocks = a.g.num_blocks;
+        p.block_size = a.g.block_size;
+        p.num_query_tokens = a.num_query_tokens;
+        p.max_query_len = a.max_query_len;
+        p.scale_log2 = a.g.scale_log2;
+        p.lse = a.g.lse;
+        p.max_context_len = a.max_context_len;
+        return launch_cross_rows(p, group, a.num_query_tokens, a.max_query_len, stream);
+    }
     const int tile_rows = (int64_t)a.max_query_len * group <= 64 ? 64 : 128;
     cross_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, tile_rows / group, ctas);
     cudaError_t e = cudaGetLastError();

@@ -209,10 +209,15 @@ struct PrefillArgs {
     int num_query_tokens;      // rows of q and out: every sequence's rows must lie in [0, this)
     int max_query_len;         // the launch covers this many rows per sequence
     float scale_log2;
+    float* lse;                // pa_cross_attention: [rows][num_heads] or null
+    int max_context_len;       // pa_cross_attention: bound of context_lens
 };
 
 cudaError_t launch_prefill(const PrefillArgs& a, int group, int num_query_tokens, int max_query_len,
                            cudaStream_t stream);
+// pa_cross_attention with many query rows, on the same kernel without the causal limit (a.sched needed).
+cudaError_t launch_cross_rows(const PrefillArgs& a, int group, int num_query_tokens, int max_query_len,
+                              cudaStream_t stream);
 
 // Whole-block copies between two pools, either of which may be pinned host memory
 // (addressed through its device mapping).

@@ -40,6 +40,9 @@
 // read it out, and its S only after the previous P.V.
 // Every wait is bounded; on expiry the CTA raises PA_DEV_WAIT_TIMEOUT, drains its own
 // copies and MMAs, frees its tensor memory and returns.
+// With CROSS set the same kernel runs pa_cross_attention where there are many query rows:
+// no causal limit, so a sequence's context and its query rows have nothing to do with each
+// other, and the log-sum-exp of each row on request.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -172,7 +175,8 @@ __device__ __forceinline__ void get_item(const volatile int* p, Item& it)
     it.nqt = p[9]; it.nA = p[10]; it.nB = p[11]; it.ntiles = p[12]; it.bad = false;
 }
 
-template <int G>
+// CROSS: every query attends to all L tokens of its sequence, whatever its place (pa_cross_attention).
+template <int G, bool CROSS>
 __device__ __forceinline__ bool item_geom(const PrefillArgs& a, int npairs, int item, Item& it)
 {
     constexpr int T = kM / G;
@@ -191,18 +195,23 @@ __device__ __forceinline__ bool item_geom(const PrefillArgs& a, int npairs, int 
     it.n = q1 - it.q0;
     it.L = __ldg(a.context_lens + it.s);
     const int Lcap = a.max_blocks_per_seq * a.block_size;
-    it.bad = it.q0 < 0 || q1 > a.num_query_tokens || it.n < 0 || it.n > a.max_query_len || it.L < it.n ||
-             it.L > Lcap;
+    it.bad = it.q0 < 0 || q1 > a.num_query_tokens || it.n < 0 || it.n > a.max_query_len || it.L > Lcap ||
+             (CROSS ? it.L < 0 || it.L > a.max_context_len : it.L < it.n);
     it.t_lo0 = it.pair * kQT * T;
-    if (it.bad || it.t_lo0 >= it.n) return false;
+    if (it.bad || it.t_lo0 >= it.n || (CROSS && it.L == 0)) return false;
     it.nqt = it.t_lo0 + T < it.n ? 2 : 1;
-    it.nA = (it.L - it.n + min(it.n, it.t_lo0 + T) - 1) / kN + 1;
-    it.nB = it.nqt > 1 ? (it.L - it.n + min(it.n, it.t_lo0 + 2 * T) - 1) / kN + 1 : 0;
+    if constexpr (CROSS) {
+        it.nA = (it.L + kN - 1) / kN;
+        it.nB = it.nqt > 1 ? it.nA : 0;
+    } else {
+        it.nA = (it.L - it.n + min(it.n, it.t_lo0 + T) - 1) / kN + 1;
+        it.nB = it.nqt > 1 ? (it.L - it.n + min(it.n, it.t_lo0 + 2 * T) - 1) / kN + 1 : 0;
+    }
     it.ntiles = it.nqt > 1 ? it.nB : it.nA;
     return true;
 }
 
-template <int G>
+template <int G, bool CROSS>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant__ CUtensorMap tmap_q,
                       const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
@@ -279,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     item = a.sched ? (int)atomicAdd(a.sched, 1u) : (claimed == 0 ? (int)blockIdx.x : nitems);
                     ++claimed;
                     if (item >= nitems) break;
-                    if (item_geom<G>(a, npairs, item, it)) break;
+                    if (item_geom<G, CROSS>(a, npairs, item, it)) break;
                     if (it.bad && it.pair == 0 && it.kvh == 0) atomicOr(a.status, PA_DEV_BAD_CONTEXT);
                 }
                 // hand it out (or the end, as -1) once every reader is done with the slot's last item
@@ -529,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 get_item(slot_k, it);
                 ntq = qt == 0 ? it.nA : it.nB;
                 const int tq = it.t_lo0 + qt * T + t_local;
-                lim = (t_local < T && tq < it.n) ? (it.L - it.n + tq) : -1;
+                lim = (t_local < T && tq < it.n) ? (CROSS ? it.L - 1 : it.L - it.n + tq) : -1;
                 jz = (it.L % kN != 0 && (it.L - 1) / kN < ntq) ? (it.L - 1) / kN : -1;
             }
             if (ntq == 0) {
@@ -685,6 +694,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after_sync();
             l += *xslot((xc - 1) & 1, half ^ 1);
             const float inv = l > 0.f ? 1.f / l : 0.f;
+            if constexpr (CROSS) {
+                if (a.lse && valid_row && half == 0)
+                    a.lse[(size_t)(it.q0 + tq) * a.num_heads + (size_t)it.kvh * G + g] =
+                        (m_used + log2f(l)) * 0.6931471805599453f;
+            }
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 uint32_t o[32];
@@ -737,24 +751,25 @@ cudaError_t q_tensor_map(CUtensorMap* out, const void* q, int num_tokens, int nu
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int G>
+template <int G, bool CROSS>
 cudaError_t launch_g(const PrefillArgs& a, int num_query_tokens, int max_query_len, cudaStream_t stream)
 {
     CUtensorMap tq, tk, tv;
     cudaError_t e = q_tensor_map(&tq, a.q, num_query_tokens, a.num_heads, G);
     if (e != cudaSuccess) return e;
     const uint64_t rows = (uint64_t)a.num_blocks * a.num_kv_heads * a.block_size;
-    if ((e = tensor_map(&tk, a.k_cache, rows, kD, kBox)) != cudaSuccess) return e;
-    if ((e = tensor_map(&tv, a.v_cache, rows, kD, kBox)) != cudaSuccess) return e;
+    auto map = CROSS ? encode_pool_map : tensor_map;
+    if ((e = map(&tk, a.k_cache, rows, kD, kBox)) != cudaSuccess) return e;
+    if ((e = map(&tv, a.v_cache, rows, kD, kBox)) != cudaSuccess) return e;
     // the kernel's attributes, set once per device (setting them twice is harmless, so
     // two threads racing to the first call need no lock)
     static std::atomic<bool> attr_done[64] = {};
     int dev = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     if (!attr_done[dev & 63].load()) {
-        e = cudaFuncSetAttribute(prefill_tc_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        e = cudaFuncSetAttribute(prefill_tc_kernel<G, CROSS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return e;
-        e = cudaFuncSetAttribute(prefill_tc_kernel<G>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+        e = cudaFuncSetAttribute(prefill_tc_kernel<G, CROSS>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
         if (e != cudaSuccess) return e;
         attr_done[dev & 63].store(true);
     }
@@ -769,8 +784,40 @@ cudaError_t launch_g(const PrefillArgs& a, int num_query_tokens, int max_query_l
     const long long nitems = (long long)npairs * a.num_seqs * a.num_kv_heads;
     if (nitems > INT32_MAX) return cudaErrorInvalidValue;
     const int grid = a.sched ? (int)std::min<long long>(nitems, sms) : (int)nitems;
-    prefill_tc_kernel<G><<<grid, kThreads, kSmem, stream>>>(a, tq, tk, tv, npairs);
+    prefill_tc_kernel<G, CROSS><<<grid, kThreads, kSmem, stream>>>(a, tq, tk, tv, npairs);
     return cudaGetLastError();
+}
+
+}  // namespace
+
+namespace {
+
+template <bool CROSS>
+cudaError_t launch_group_of(const PrefillArgs& a, int group, int num_query_tokens, int max_query_len, cudaStream_t stream)
+{
+    if (a.num_seqs == 0 || max_query_len == 0 || num_query_tokens == 0) return cudaSuccess;
+    switch (group) {
+        case 1: return launch_g<1, CROSS>(a, num_query_tokens, max_query_len, stream);
+        case 2: return launch_g<2, CROSS>(a, num_query_tokens, max_query_len, stream);
+        case 4: return launch_g<4, CROSS>(a, num_query_tokens, max_query_len, stream);
+        case 8: return launch_g<8, CROSS>(a, num_query_tokens, max_query_len, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+// Rows of sequences without tokens: zero, and -inf.  A CTA per sequence, which also zeroes the item counter.
+__global__ void __launch_bounds__(256) cross_empty_kernel(const PrefillArgs a)
+{
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.sched = 0u;
+    for (int s = blockIdx.x; s < a.num_seqs; s += gridDim.x) {
+        const int q0 = __ldg(a.q_start + s), q1 = __ldg(a.q_start + s + 1);
+        if (__ldg(a.context_lens + s) != 0 || q0 < 0 || q1 > a.num_query_tokens || q1 - q0 > a.max_query_len) continue;
+        const int64_t n = (int64_t)(q1 - q0) * a.num_heads;
+        uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (size_t)q0 * a.num_heads * kD);
+        for (int64_t i = threadIdx.x; i < n * (kD / 8); i += 256) out[i] = make_uint4(0, 0, 0, 0);
+        if (a.lse)
+            for (int64_t i = threadIdx.x; i < n; i += 256) a.lse[(size_t)q0 * a.num_heads + i] = -INFINITY;
+    }
 }
 
 }  // namespace
@@ -778,14 +825,15 @@ cudaError_t launch_g(const PrefillArgs& a, int num_query_tokens, int max_query_l
 cudaError_t launch_prefill(const PrefillArgs& a, int group, int num_query_tokens, int max_query_len,
                            cudaStream_t stream)
 {
-    if (a.num_seqs == 0 || max_query_len == 0 || num_query_tokens == 0) return cudaSuccess;
-    switch (group) {
-        case 1: return launch_g<1>(a, num_query_tokens, max_query_len, stream);
-        case 2: return launch_g<2>(a, num_query_tokens, max_query_len, stream);
-        case 4: return launch_g<4>(a, num_query_tokens, max_query_len, stream);
-        case 8: return launch_g<8>(a, num_query_tokens, max_query_len, stream);
-        default: return cudaErrorInvalidValue;
-    }
+    return launch_group_of<false>(a, group, num_query_tokens, max_query_len, stream);
+}
+
+cudaError_t launch_cross_rows(const PrefillArgs& a, int group, int num_query_tokens, int max_query_len,
+                              cudaStream_t stream)
+{
+    cross_empty_kernel<<<std::min(a.num_seqs, 1024), 256, 0, stream>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_group_of<true>(a, group, num_query_tokens, max_query_len, stream);
 }
 
 }  // namespace pa
