@@ -616,24 +616,25 @@ __global__ void __launch_bounds__(128) group_merge_kernel(const GroupArgs a)
     }
 }
 
-// pa_cross_attention's plan: one entry per (sequence, tile of 128 / G query tokens, chunk of
-// its tokens), the tiles of a chunk next to each other (they read the same K/V), and the
-// query rows of sequences with several chunks for the merge.  The chunk length is the work
-// (tokens x tiles x kv heads) over twice the resident CTAs, at least 256 tokens.
+// pa_cross_attention's plan: one entry per (sequence, tile of query tokens, chunk of its tokens), the tiles
+// of a chunk next to each other (they read the same K/V), and the query rows of sequences with several
+// chunks for the merge.
 constexpr int kPlanThreads = 1024;
 
-__global__ void __launch_bounds__(kPlanThreads, 1) cross_plan_kernel(const CrossArgs a, int T, int ctas)
+__global__ void __launch_bounds__(kPlanThreads, 1) cross_plan_kernel(const CrossArgs a, int T, int D, int ctas)
 {
-    __shared__ unsigned long long s_work;
-    __shared__ unsigned s_items, s_merges;
+    __shared__ unsigned s_steps, s_rows, s_class[kLenClasses], s_merges, s_over;
+    __shared__ int s_longest;
     __shared__ int s_q0[kPlanThreads], s_n[kPlanThreads], s_len[kPlanThreads];
     pdl_launch_dependents();
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, S = a.num_seqs;
     const int cap = min(a.max_context_len, (int)min((long long)a.g.max_blocks_per_seq * a.g.block_size, 0x7fffffffll));
     const bool split = a.max_chunks > 1;
+    if (tid < kLenClasses) s_class[tid] = 0;
     if (tid == 0) {
-        s_work = 0;
-        s_items = s_merges = 0;
+        s_steps = s_rows = 0;
+        s_merges = s_over = 0;
+        s_longest = 0;
     }
     // rows and tokens of sequence s; no rows where its data is bad
     auto load = [&](int s, bool flag) {
@@ -643,75 +644,117 @@ __global__ void __launch_bounds__(kPlanThreads, 1) cross_plan_kernel(const Cross
         s_q0[tid] = q0;
         s_n[tid] = bad ? 0 : q1 - q0;
         s_len[tid] = L;
-        return bad ? 0ull : (unsigned long long)((q1 - q0 + T - 1) / T) * L;
     };
-    const bool one = a.num_seqs <= kPlanThreads;  // a batch this small is loaded once
-    unsigned long long work = 0;
-    if (split || !one)
-        for (int s = tid; s < a.num_seqs; s += kPlanThreads) work += load(s, true);
-    else if (tid < a.num_seqs)
-        load(tid, true);
+    const bool one = S <= kPlanThreads;  // a batch this small is loaded once
+    // f(rows, tokens) for this thread's sequences
+    auto each = [&](bool first, auto f) {
+        for (int s = tid; s < S; s += kPlanThreads) {
+            if (first || !one) load(s, first);
+            if (s_n[tid] > 0) f(s_n[tid], s_len[tid]);
+        }
+    };
+    // (sums may wrap for absurd batches: the chunk length is then a poor one, and no more)
+    unsigned steps = 0, nrows = 0;
+    int longest = 0;
+    each(true, [&](int rows, int L) {
+        steps += (unsigned)((rows + T - 1) / T) * (unsigned)((L + kTok - 1) / kTok);
+        nrows += (unsigned)rows;
+        longest = max(longest, L);
+    });
+    __syncthreads();
+    int chunk = 0;
     if (split) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) work += __shfl_xor_sync(0xffffffffu, work, o);
+        longest = __reduce_max_sync(0xffffffffu, longest);
+        steps = __reduce_add_sync(0xffffffffu, steps);
+        nrows = __reduce_add_sync(0xffffffffu, nrows);
+        if (lane == 0 && nrows) {
+            atomicAdd(&s_steps, steps);
+            atomicAdd(&s_rows, nrows);
+            atomicMax(&s_longest, longest);
+        }
         __syncthreads();
-        if (lane == 0 && work) atomicAdd(&s_work, work);
+        chunk = plan_chunk((float)s_steps * (float)a.g.num_kv_heads, ctas, s_longest, (float)s_rows * (float)a.g.num_heads,
+                           a.max_chunks, D, false);
+    }
+    // tokens of a sequence's chunks, all the same but the last, and their number
+    auto chunks_of = [&](int L, int& per) {
+        if (!split || L <= chunk) {
+            per = max(L, 1);
+            return 1;
+        }
+        const int want = (L + chunk - 1) / chunk;
+        per = ((L + want - 1) / want + kTok - 1) / kTok * kTok;
+        return (L + per - 1) / per;
+    };
+    const int top = split ? max(chunk, 1) : max(a.max_context_len, 1);
+    each(false, [&](int rows, int L) {
+        int per;
+        const int n = chunks_of(L, per);
+        atomicAdd(&s_class[len_class(per, top)], (unsigned)(n * ((rows + T - 1) / T)));
+    });
+    __syncthreads();
+    if (warp == 0) {
+        const unsigned c = lane < kLenClasses ? s_class[lane] : 0u;
+        unsigned x = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane < kLenClasses) s_class[lane] = x - c;
+        if (lane == 31) s_over = x;  // all entries
     }
     __syncthreads();
-    const int share = (int)fminf((float)s_work * (float)a.g.num_kv_heads / (2.f * (float)ctas), 1e9f);
-    const int least = (a.max_context_len + a.max_chunks - 1) / a.max_chunks;
-    const int chunk = (max(max(share, least), 256) + kTok - 1) / kTok * kTok;
+    const unsigned entries = s_over;
     GroupItem* items = const_cast<GroupItem*>(a.g.items);
     uint2* merges = const_cast<uint2*>(a.g.merge_list);
-    for (int s0 = 0; s0 < a.num_seqs; s0 += kPlanThreads) {
+    const unsigned room = (unsigned)a.g.max_entries, mroom = (unsigned)a.g.max_merges;
+    for (int s0 = 0; s0 < S; s0 += kPlanThreads) {
         if (!one) {
             __syncthreads();
-            if (s0 + tid < a.num_seqs) load(s0 + tid, false);
+            if (s0 + tid < S) load(s0 + tid, false);
             __syncthreads();
         }
-        for (int i = warp; i < min(kPlanThreads, a.num_seqs - s0); i += kPlanThreads / 32) {
+        for (int i = warp; i < min(kPlanThreads, S - s0); i += kPlanThreads / 32) {
             const int q0 = s_q0[i], rows = s_n[i], L = s_len[i];
             if (rows == 0) continue;
             const int tiles = (rows + T - 1) / T;
-            const int want = L <= chunk ? 1 : (L + chunk - 1) / chunk;
-            const int per = max(1, ((L + want - 1) / want + kTok - 1) / kTok) * kTok;
-            const int nch = L <= per ? 1 : (L + per - 1) / per;
+            int per;
+            const int nch = chunks_of(L, per);
             unsigned i0 = 0, m0 = 0;
             if (lane == 0) {
-                i0 = atomicAdd(&s_items, (unsigned)(tiles * nch));
+                i0 = atomicAdd(&s_class[len_class(per, top)], (unsigned)(tiles * nch));
                 m0 = nch > 1 ? atomicAdd(&s_merges, (unsigned)rows) : 0u;
             }
             i0 = __shfl_sync(0xffffffffu, i0, 0);
             m0 = __shfl_sync(0xffffffffu, m0, 0);
             // rows listed twice (q_start running backwards elsewhere) can ask for more than there is room for
-            if (i0 + tiles * nch > (unsigned)a.g.max_entries || (nch > 1 && m0 + rows > (unsigned)a.g.max_merges)) {
-                if (lane == 0) atomicOr(a.g.status, PA_DEV_BAD_CONTEXT);
-                for (unsigned k = i0 + lane; k < min(i0 + tiles * nch, (unsigned)a.g.max_entries); k += 32)
-                    items[k] = GroupItem{0, 0, 0, 0, 0, 0, {0, 0}};
-                for (unsigned k = m0 + lane; nch > 1 && k < min(m0 + rows, (unsigned)a.g.max_merges); k += 32)
-                    merges[k] = make_uint2((unsigned)q0, 0u);
-                continue;
-            }
+            const bool fits = i0 + tiles * nch <= room && (nch == 1 || m0 + rows <= mroom);
+            if (!fits && lane == 0) atomicOr(a.g.status, PA_DEV_BAD_CONTEXT);
             for (int k = lane; k < tiles * nch; k += 32) {
+                if (i0 + k >= room) break;
                 const int ch = nch > 1 ? k / tiles : 0, tile = k - ch * tiles;
                 GroupItem it{};
-                it.table_row = s0 + i;
-                it.row0 = q0 + tile * T;
-                it.members = min(T, rows - tile * T);
-                it.chunk = nch > 1 ? ch : -1;
-                it.kv0 = ch * per;
-                it.kvlen = min(per, L - ch * per);
+                if (fits) {
+                    it.table_row = s0 + i;
+                    it.row0 = q0 + tile * T;
+                    it.members = min(T, rows - tile * T);
+                    it.chunk = nch > 1 ? ch : -1;
+                    it.kv0 = ch * per;
+                    it.kvlen = min(per, L - ch * per);
+                }
                 items[i0 + k] = it;
             }
             if (nch > 1)
-                for (int k = lane; k < rows; k += 32) merges[m0 + k] = make_uint2((unsigned)(q0 + k), (unsigned)nch);
+                for (int k = lane; k < rows; k += 32)
+                    if (m0 + k < mroom) merges[m0 + k] = make_uint2((unsigned)(q0 + k), fits ? (unsigned)nch : 0u);
         }
     }
     __syncthreads();
     if (tid == 0) {
         unsigned* counts = const_cast<unsigned*>(a.g.counts);
-        counts[0] = min(s_items, (unsigned)a.g.max_entries);
-        counts[1] = min(s_merges, (unsigned)a.g.max_merges);
+        counts[0] = min(entries, room);
+        counts[1] = min(s_merges, mroom);
     }
 }
 
@@ -810,7 +853,7 @@ cudaError_t launch_cross(const CrossArgs& a, int head_dim, int group, cudaStream
         return launch_cross_rows(p, group, a.num_query_tokens, a.max_query_len, stream);
     }
     const int tile_rows = (int64_t)a.max_query_len * group <= 64 ? 64 : 128;
-    cross_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, tile_rows / group, ctas);
+    cross_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, tile_rows / group, head_dim, ctas);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     if ((e = launch_group(a.g, head_dim, group, tile_rows, ctas, stream)) != cudaSuccess) return e;

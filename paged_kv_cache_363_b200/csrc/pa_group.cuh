@@ -73,6 +73,32 @@ inline int group_max_chunks(int64_t max_len, int64_t rows, int group, int num_kv
     return (int)(n < 32 ? n : 32);
 }
 
+#ifdef __CUDACC__
+// The chunk length of a plan.  Split or not, from four sums: `steps` (tiles of rows x tiles of 64 tokens x kv
+// heads), the longest table, and the (row, head) pairs.  Unsplit, the time is the longest table's or the mean
+// load's, at about 1 us a step; split into the mean load of a CTA (256 tokens at least), that load's and the
+// partial states' (written and read at 5 TB/s), and 4 us where a split brings a merge with it.
+// (Splitting every batch into two units per CTA cost 16 sequences x 64 rows x 1500 tokens 90 us, 60 unsplit.)
+__device__ __forceinline__ int plan_chunk(float steps, int ctas, int longest, float pairs, int max_chunks, int D, bool merge_anyway)
+{
+    const float load = steps / (float)ctas;
+    const int least = (longest + max_chunks - 1) / max_chunks;
+    const int c = (max(max((int)fminf(64.f * load, 1e9f), least), 256) + 63) / 64 * 64;
+    if (c >= longest) return max(longest, 1);
+    const float whole = fmaxf((float)longest * (1.f / 64.f), load);
+    const float states = pairs * ceilf((float)longest / (float)c);
+    const float parts = fmaxf((float)c * (1.f / 64.f), load) + states * (float)D * (8.f / 5e6f) + (merge_anyway ? 0.f : 4.f);
+    return whole <= parts ? longest : c;
+}
+
+// Entries go longest first, by sixteenths of the chunk: a CTA's units then are one of every length.
+constexpr int kLenClasses = 16;
+__device__ __forceinline__ int len_class(int kvlen, int chunk)
+{
+    return kLenClasses - 1 - min(kLenClasses - 1, (int)((float)kvlen / (float)chunk * kLenClasses));
+}
+#endif
+
 // CTAs of the kernel resident on the device at once.
 int group_resident_ctas(int sms);
 

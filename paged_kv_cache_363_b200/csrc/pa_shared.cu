@@ -42,19 +42,18 @@ __device__ __forceinline__ OwnItem load_own(const OwnItem* items, unsigned i, un
 //     tokens than any member's context).  A bad one raises PA_DEV_BAD_CONTEXT and is not
 //     shared: its rows attend to all their tokens on their own, which is the same result.
 //  2. Entries of the shared tokens: (tile of rows, chunk), a chunk's tiles next to each other.
-//     The chunk length is the work over twice the resident CTAs, at least 256 tokens.
 //  3. Entries of the own tokens: a row, or one of its parts, the longer half of the entries
 //     first.  A part is half a warp's share of all own tokens, at least 256 (joining a row's
 //     parts costs some 4 us) and as many as keep the row within its partial states.
 // A batch of up to 1024 rows keeps its per-row values in shared memory: the plan is on the
 // critical path, and most of it was trips to L2.
-__global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const SharedArgs a, int T, int group_ctas, int own_warps)
+__global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const SharedArgs a, int T, int D, int group_ctas, int own_warps)
 {
     __shared__ int s_listed[kPlanThreads], s_ctx[kPlanThreads], s_lead[kPlanThreads], s_states[kPlanThreads];
     __shared__ int s_rows[kPlanThreads], s_start[kPlanThreads + 1], s_len[kPlanThreads], s_ok[kPlanThreads];
-    __shared__ unsigned long long s_work, s_own;
+    __shared__ unsigned s_steps, s_members, s_own, s_class[kLenClasses];
     __shared__ unsigned s_items, s_big, s_front, s_back;
-    __shared__ int s_bad;
+    __shared__ int s_bad, s_longest;
     pdl_launch_dependents();
     const int B = a.g.block_size, S = a.num_seqs, NG = a.num_groups, R = a.num_group_rows;
     const int bshift = B == 16 ? 4 : 5;
@@ -69,10 +68,11 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
     const int* start = small ? s_start : a.group_start;
     const int* lens = small ? s_len : a.shared_lens;
     if (tid == 0) {
-        s_work = s_own = 0;
+        s_steps = s_members = s_own = 0;
         s_items = s_big = s_front = s_back = 0;
-        s_bad = 0;
+        s_bad = s_longest = 0;
     }
+    if (tid < kLenClasses) s_class[tid] = 0;
     if (small) {
         // everything the plan reads, in one trip
         const int r = tid < R ? __ldg(a.group_rows + tid) : 0;
@@ -119,24 +119,50 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
         if (lane == 0) {
             group_ok[g] = ok && n > 0 && r1 > r0;
             if (!ok) atomicOr(a.g.status, PA_DEV_BAD_CONTEXT);
-            else if (n > 0) atomicAdd(&s_work, (unsigned long long)((r1 - r0 + T - 1) / T) * n);
+            else if (n > 0) {
+                atomicAdd(&s_steps, (unsigned)((r1 - r0 + T - 1) / T) * (unsigned)((n + 63) / 64));
+                atomicAdd(&s_members, (unsigned)(r1 - r0));
+                atomicMax(&s_longest, n);
+            }
         }
     }
     __syncthreads();
-    if (s_work > 0) {
-        const int share = (int)fminf((float)s_work * (float)a.g.num_kv_heads / (2.f * (float)group_ctas), 1e9f);
-        const int least = (a.max_shared_len + a.max_chunks - 1) / a.max_chunks;
-        const int chunk = (max(max(share, least), 256) + 63) / 64 * 64;
+    if (s_steps > 0) {
+        const int chunk = plan_chunk((float)s_steps * (float)a.g.num_kv_heads, group_ctas, s_longest,
+                                     (float)s_members * (float)a.g.num_heads, a.max_chunks, D, true);
+        auto chunks_of = [&](int n, int& per) {
+            const int want = (n + chunk - 1) / chunk;
+            per = ((n + want - 1) / want + 63) / 64 * 64;
+            return (n + per - 1) / per;
+        };
+        for (int g = tid; g < ngroups; g += kPlanThreads)
+            if (group_ok[g]) {
+                int per;
+                const int nch = chunks_of(lens[g], per);
+                atomicAdd(&s_class[len_class(per, chunk)], (unsigned)(nch * ((start[g + 1] - start[g] + T - 1) / T)));
+            }
+        __syncthreads();
+        if (warp == 0) {
+            const unsigned c = lane < kLenClasses ? s_class[lane] : 0u;
+            unsigned x = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            if (lane < kLenClasses) s_class[lane] = x - c;
+            if (lane == 31) s_items = x;
+        }
+        __syncthreads();
         GroupItem* items = const_cast<GroupItem*>(a.g.items);
         for (int g = warp; g < ngroups; g += kPlanThreads / 32) {
             if (!group_ok[g]) continue;
             const int r0 = start[g], r1 = start[g + 1], n = lens[g];
             const int tiles = (r1 - r0 + T - 1) / T;
-            const int want = (n + chunk - 1) / chunk;
-            const int per = ((n + want - 1) / want + 63) / 64 * 64;
-            const int nch = (n + per - 1) / per;
+            int per;
+            const int nch = chunks_of(n, per);
             unsigned i0 = 0;
-            if (lane == 0) i0 = atomicAdd(&s_items, (unsigned)(tiles * nch));
+            if (lane == 0) i0 = atomicAdd(&s_class[len_class(per, chunk)], (unsigned)(tiles * nch));
             i0 = __shfl_sync(0xffffffffu, i0, 0);
             const int first = rows[r0];
             for (int i = lane; i < tiles * nch; i += 32) {
@@ -158,10 +184,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
         }
         __syncthreads();
     }
-    unsigned long long tok = 0;
-    for (int s = tid; s < S; s += kPlanThreads) tok += (unsigned long long)(ctx[s] - lead_blocks[s] * B);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) tok += __shfl_xor_sync(0xffffffffu, tok, o);
+    unsigned tok = 0;
+    for (int s = tid; s < S; s += kPlanThreads) tok += (unsigned)(ctx[s] - lead_blocks[s] * B);
+    tok = __reduce_add_sync(0xffffffffu, tok);
     if (lane == 0 && tok) atomicAdd(&s_own, tok);
     __syncthreads();
     const int share = (int)fminf((float)s_own * (float)a.g.num_kv_heads / (2.f * (float)own_warps), 1e9f);
@@ -628,7 +653,7 @@ cudaError_t launch_shared_dg(const SharedArgs& a, cudaStream_t stream)
     args.wait_first = shares ? 0 : 1;
     const int64_t units = (int64_t)a.num_seqs * a.max_parts * a.g.num_kv_heads;
     const unsigned grid = (unsigned)std::min<int64_t>((units + kOwnWarps - 1) / kOwnWarps, 2LL * sms);
-    shared_plan_kernel<<<1, kPlanThreads, 0, stream>>>(args, tile_rows / G, gctas, 2 * sms * kOwnWarps);
+    shared_plan_kernel<<<1, kPlanThreads, 0, stream>>>(args, tile_rows / G, D, gctas, 2 * sms * kOwnWarps);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (shares && (e = launch_group(args.g, D, G, tile_rows, gctas, stream)) != cudaSuccess) return e;
     return launch_pdl(shared_own_kernel<D, G>, dim3(grid), dim3(kOwnThreads), (size_t)C::SMEM, stream, args);
