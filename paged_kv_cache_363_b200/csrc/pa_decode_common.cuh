@@ -272,6 +272,74 @@ __device__ __forceinline__ void finish_unit_warp(const DecodeArgs& a, const floa
     }
 }
 
+// The row statistics of an unsplit unit's heads from the consumer warps' states, summed in the order of
+// finish_unit_warp: the maxima and the reciprocals of the softmax sums.
+template <int G, int NCW>
+__device__ __forceinline__ void unit_stats(const float* mg_m, const float* mg_l, int rot, float (&hm)[G], float (&hinv)[G])
+{
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        float M = -INFINITY, den = 0.f;
+#pragma unroll
+        for (int w = 0; w < NCW; ++w) M = fmaxf(M, mg_m[w * G + g]);
+#pragma unroll
+        for (int j = 0; j < NCW; ++j) {
+            const int w = (rot + j) % NCW;
+            const float mj = mg_m[w * G + g];
+            if (mj != -INFINITY) den = fmaf(exp2f(mj - M), mg_l[w * G + g], den);
+        }
+        hm[g] = M;
+        hinv[g] = den > 0.f ? 1.f / den : 0.f;
+    }
+}
+
+// scores[i] += sum over heads of 2^(logit - max) / sum; the last token of the context (L - 1) has no history
+// and is set.  The heads are added in order.  One thread's tokens lo + tid + k * NT (k < UN) below hi: load()
+// asks for their logits and scores, which do not need the statistics that add() does.
+template <int G, int NT, int UN>
+struct WeightTokens {
+    float x[UN][G], old[UN];
+
+    __device__ __forceinline__ void load(const float* lg, const float* sc, int lo, int hi, int tid)
+    {
+#pragma unroll
+        for (int k = 0; k < UN; ++k) {
+            const int i = lo + tid + k * NT;
+            if (i >= hi) continue;
+            const float* p = lg + (size_t)i * G;
+            if constexpr (G == 1) {
+                x[k][0] = p[0];
+            } else if constexpr (G == 2) {
+                const float2 v = *reinterpret_cast<const float2*>(p);
+                x[k][0] = v.x;
+                x[k][1] = v.y;
+            } else {
+#pragma unroll
+                for (int g = 0; g < G; g += 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(p + g);
+                    x[k][g] = v.x;
+                    x[k][g + 1] = v.y;
+                    x[k][g + 2] = v.z;
+                    x[k][g + 3] = v.w;
+                }
+            }
+            old[k] = sc[i];
+        }
+    }
+    __device__ __forceinline__ void add(float* sc, int lo, int hi, int L, int tid, const float* hm, const float* hinv)
+    {
+#pragma unroll
+        for (int k = 0; k < UN; ++k) {
+            const int i = lo + tid + k * NT;
+            if (i >= hi) continue;
+            float w = 0.f;
+#pragma unroll
+            for (int g = 0; g < G; ++g) w = fmaf(exp2f(x[k][g] - hm[g]), hinv[g], w);
+            sc[i] = i == L - 1 ? w : old[k] + w;
+        }
+    }
+};
+
 // Log-sum-exp merge of the partitions of the split sequences the plan listed:
 // M = max_p m_p, out = sum_p 2^(m_p - M) acc_p / sum_p 2^(m_p - M) l_p, per
 // (sequence, query head) row.  `nwr` warps share a row (1, 2 or 4; a CTA of four

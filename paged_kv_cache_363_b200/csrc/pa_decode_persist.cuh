@@ -149,6 +149,7 @@ __global__ void __launch_bounds__(Persist<Cons, BS>::THREADS, 2)
     // only its unit producer waits for the plan, before its second unit.  Every other
     // CTA waits here; the plan kernel's list and counters are visible after the wait.
     const bool early = (int)blockIdx.x < a.first_wave;
+    const bool planless = MODE == kModeScores && a.planless != 0;  // every unit is in the first wave: no plan was made
     if (!early) pdl_wait_primary();
 
     auto slot = [&](int k) { return smem + P::OFF_SLOT + (k % UR) * P::SLOT_BYTES; };
@@ -167,7 +168,7 @@ __global__ void __launch_bounds__(Persist<Cons, BS>::THREADS, 2)
         auto plan_ready = [&]() { nunits = __ldcg(a.plan + 1) * (unsigned)a.num_kv_heads; };
         if (early) {
             const int s0 = (int)(blockIdx.x / (unsigned)a.num_kv_heads);
-            e_first = make_uint2((unsigned)s0 << 11, (unsigned)clamped_context(a, s0, B, false));
+            e_first = make_uint2((unsigned)s0 << 11, (unsigned)clamped_context(a, s0, B, planless));
         } else {
             e_first = __ldcg(a.plan_list + blockIdx.x / (unsigned)a.num_kv_heads);
             plan_ready();
@@ -178,6 +179,7 @@ __global__ void __launch_bounds__(Persist<Cons, BS>::THREADS, 2)
         // it happens while the CTAs still finish their last units, off the kernel's
         // critical path.  Lane 0 only.
         auto leave = [&]() {
+            if (planless) return;
             if (atomicAdd(a.plan + 4, 1u) == gridDim.x - 1) {
                 a.plan[0] = 0u;
                 a.plan[4] = 0u;
@@ -198,7 +200,9 @@ __global__ void __launch_bounds__(Persist<Cons, BS>::THREADS, 2)
             UnitInfo* info = slot_info(k);
             // the first unit of CTA b is unit b; later ones come from the counter
             unsigned u = blockIdx.x;
-            if (k > 0) {
+            if (planless && k > 0) {
+                u = 0u;  // (nunits is 0: the end)
+            } else if (k > 0) {
                 if (k == 1 && early) {
                     pdl_wait_primary();
                     plan_ready();
@@ -359,12 +363,32 @@ __global__ void __launch_bounds__(Persist<Cons, BS>::THREADS, 2)
                     break;
                 }
                 const bool split = (info->flags & kSplitUnit) != 0;
-                finish_unit_warp<T, D, G, NCW, MODE == kModeScores>(
-                    a, mg_m, mg_l, mg_acc, info->s, info->kvh, info->part, split, first % NCW, lane);
+                finish_unit_warp<T, D, G, NCW, MODE == kModeScores>(a, mg_m, mg_l, mg_acc, info->s, info->kvh,
+                                                                    info->part, split, first % NCW, lane);
+                // Without a plan this is the CTA's only unit, and the whole sequence's: the weights follow here.
+                // (With one, a second kernel adds them: a warp that left the stream for the 3 us that takes held
+                // the ring up, 69 -> 81 us on 128 sequences of 16 to 4096 tokens.)
+                const bool score = planless && L > 0;
+                float hm[G], hinv[G];
+                const float* lg = nullptr;
+                float* sc = nullptr;
+                if (score) {
+                    unit_stats<G, NCW>(mg_m, mg_l, first % NCW, hm, hinv);
+                    const size_t row = (size_t)info->s * a.num_kv_heads + info->kvh;
+                    lg = a.logits + row * a.max_context_len * G;
+                    sc = a.scores + row * a.score_stride;
+                }
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(mg_free);
                     mbar_arrive(&uempty[k % UR]);
+                }
+                if (score) {
+                    WeightTokens<G, 32, 2> w;
+                    for (int i = 0; i < L; i += 64) {
+                        w.load(lg, sc, i, L, lane);
+                        w.add(sc, i, L, L, lane, hm, hinv);
+                    }
                 }
             }
         }
@@ -441,11 +465,18 @@ cudaError_t launch_persistent(const DecodeArgs& a, cudaStream_t stream)
     // b % Hkv of partition 0 of sequence b / Hkv without waiting for the plan.  The plan
     // grows an automatic partition only when the tokens of all sequences exceed
     // 4 x partition x CTAs, which the bound num_seqs x max_context_len rules out here.
+    args.planless = MODE == kModeScores && a.num_partitions == 1 && units <= ctas ? 1 : 0;
     const bool fixed_partition =
         !a.adaptive || (int64_t)a.num_seqs * a.max_context_len <= 4LL * args.partition_blocks * BS * (int64_t)grid;
     const int64_t pairs0 = (int64_t)a.num_seqs * a.num_kv_heads;
-    args.first_wave = fixed_partition ? (int)(pairs0 < (int64_t)grid ? pairs0 : (int64_t)grid) : 0;
+    args.first_wave = fixed_partition || args.planless ? (int)(pairs0 < (int64_t)grid ? pairs0 : (int64_t)grid) : 0;
 
+    if (a.was_planless) *a.was_planless = args.planless;
+    if (args.planless) {
+        // no kernel of this call comes before it, so it may not overlap the one that does
+        decode_persistent_kernel<Cons, BS, MODE><<<grid, P::THREADS, (size_t)P::SMEM, stream>>>(args, tk, tv);
+        return cudaGetLastError();
+    }
     if (a.phases & kDecodePlan) {
         // one CTA; fewer threads for small batches keep its barriers short
         const int plan_threads = a.num_seqs <= 256 ? 256 : (a.num_seqs <= 512 ? 512 : 1024);
@@ -456,7 +487,7 @@ cudaError_t launch_persistent(const DecodeArgs& a, cudaStream_t stream)
     if (!(a.phases & kDecodeRun)) return cudaSuccess;
     e = launch_pdl(decode_persistent_kernel<Cons, BS, MODE>, dim3(grid), dim3(P::THREADS), (size_t)P::SMEM, stream,
                    args, tk, tv);
-    if (e != cudaSuccess || a.num_partitions <= 1) return e;
+    if (e != cudaSuccess || a.num_partitions <= 1 || MODE == kModeScores) return e;
     return launch_merge<typename Cons::T, P::D>(args, BS, stream);
 }
 

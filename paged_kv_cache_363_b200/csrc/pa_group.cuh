@@ -83,7 +83,8 @@ __device__ __forceinline__ int plan_chunk(float steps, int ctas, int longest, fl
 {
     const float load = steps / (float)ctas;
     const int least = (longest + max_chunks - 1) / max_chunks;
-    const int c = (max(max((int)fminf(64.f * load, 1e9f), least), 256) + 63) / 64 * 64;
+    // (half of the mean where the states are joined anyway: the two CTAs of an SM even out better)
+    const int c = (max(max((int)fminf((merge_anyway ? 32.f : 64.f) * load, 1e9f), least), 256) + 63) / 64 * 64;
     if (c >= longest) return max(longest, 1);
     const float whole = fmaxf((float)longest * (1.f / 64.f), load);
     const float states = pairs * ceilf((float)longest / (float)c);

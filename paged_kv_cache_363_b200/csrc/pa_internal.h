@@ -60,6 +60,8 @@ struct DecodeArgs {
     float* logits;             // pa_decode_scores: [S][Hkv][max_context_len][G] base-2 logits
     float* scores;             // pa_decode_scores: [S][Hkv][score_stride]
     int score_stride;
+    int planless;              // pa_decode_scores: every unit has a CTA of its own, and no plan is made
+    int* was_planless;         // host side: receives the launch's choice of it
 };
 
 constexpr int kDecodePlan = 1;  // the plan kernel: work list into the workspace

@@ -136,9 +136,29 @@ def _pool_ptr(t, name):
 
 
 def _stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _launch(stream, *tensors):
+    """The stream and the addresses of a call's tensors (None stays None): CUDA, contiguous, and all on the
+    current device, whose stream and library state the call uses."""
+    import torch
+    cur = torch.cuda.current_device()
+    ptrs = []
+    for t in tensors:
+        if t is None:
+            ptrs.append(None)
+            continue
+        if t.get_device() != cur:
+            raise ValueError("every tensor must be on the current CUDA device (%d), not %s" % (cur, t.device))
+        if not t.is_contiguous():
+            raise ValueError("every tensor must be contiguous")
+        ptrs.append(t.data_ptr())
+    # the raw handle of the current stream, without a Stream object around it
+    return (torch._C._cuda_getCurrentRawStream(cur) if stream is None else stream.cuda_stream), ptrs
 
 
 # ---------------------------------------------------------------- device calls
@@ -270,13 +290,11 @@ def pa_decode_shared(out, q, k_cache, v_cache, block_tables, context_lens, group
     if workspace is None:
         need = pa_decode_shared_workspace_size(S, Hq, Hkv, D, B, int(max_context_len), int(max_shared_len), groups, n)
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    st = lib.pa_decode_shared(_dev_ptr(out, "out"), _dev_ptr(q, "q"), _dev_ptr(k_cache, "k_cache"),
-                              _dev_ptr(v_cache, "v_cache"), _dev_ptr(block_tables, "block_tables"),
-                              _dev_ptr(context_lens, "context_lens"), _dev_ptr(group_rows, "group_rows"),
-                              _dev_ptr(group_start, "group_start"), _dev_ptr(shared_lens, "shared_lens"), S, Hq, Hkv, D,
-                              B, block_tables.shape[1], NB, groups, n, int(max_context_len), int(max_shared_len),
-                              float(scale), _dev_ptr(workspace, "workspace"),
-                              workspace.numel() * workspace.element_size(), _dtype_code(q), _stream(stream))
+    handle, (*ptrs, ws) = _launch(stream, out, q, k_cache, v_cache, block_tables, context_lens, group_rows, group_start,
+                                  shared_lens, workspace)
+    st = lib.pa_decode_shared(*ptrs, S, Hq, Hkv, D, B, block_tables.shape[1], NB, groups, n, int(max_context_len),
+                              int(max_shared_len), float(scale), ws, workspace.numel() * workspace.element_size(),
+                              _dtype_code(q), handle)
     _check(st, "pa_decode_shared")
     return out
 
@@ -309,12 +327,10 @@ def pa_decode_scores(out, scores, q, k_cache, v_cache, block_tables, context_len
     if workspace is None:
         need = pa_decode_scores_workspace_size(S, Hq, Hkv, D, B, int(max_context_len), int(partition_size))
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    st = lib.pa_decode_scores(_dev_ptr(out, "out"), _dev_ptr(scores, "scores"), _dev_ptr(q, "q"),
-                              _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"),
-                              _dev_ptr(block_tables, "block_tables"), _dev_ptr(context_lens, "context_lens"), S, Hq,
-                              Hkv, D, B, block_tables.shape[1], NB, int(max_context_len), scores.shape[2],
-                              float(scale), int(partition_size), _dev_ptr(workspace, "workspace"),
-                              workspace.numel() * workspace.element_size(), _dtype_code(q), _stream(stream))
+    handle, (*ptrs, ws) = _launch(stream, out, scores, q, k_cache, v_cache, block_tables, context_lens, workspace)
+    st = lib.pa_decode_scores(*ptrs, S, Hq, Hkv, D, B, block_tables.shape[1], NB, int(max_context_len), scores.shape[2],
+                              float(scale), int(partition_size), ws, workspace.numel() * workspace.element_size(),
+                              _dtype_code(q), handle)
     _check(st, "pa_decode_scores")
     return out
 
@@ -345,13 +361,10 @@ def pa_evict(k_cache, v_cache, new_scores, new_positions, scores, positions, blo
     if workspace is None:
         need = pa_evict_workspace_size(S, Hkv, int(max_context_len))
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=k_cache.device)
-    st = lib.pa_evict(_dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"), _dev_ptr(new_scores, "new_scores"),
-                      _dev_ptr(new_positions, "new_positions"), _dev_ptr(scores, "scores"),
-                      _dev_ptr(positions, "positions"), _dev_ptr(block_tables, "block_tables"),
-                      _dev_ptr(context_lens, "context_lens"), _dev_ptr(keep_lens, "keep_lens"), int(num_recent), S,
-                      Hkv, D, B, block_tables.shape[1], NB, int(max_context_len), scores.shape[2],
-                      _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-                      _dtype_code(k_cache), _stream(stream))
+    handle, (*ptrs, ws) = _launch(stream, k_cache, v_cache, new_scores, new_positions, scores, positions, block_tables,
+                                  context_lens, keep_lens, workspace)
+    st = lib.pa_evict(*ptrs, int(num_recent), S, Hkv, D, B, block_tables.shape[1], NB, int(max_context_len),
+                      scores.shape[2], ws, workspace.numel() * workspace.element_size(), _dtype_code(k_cache), handle)
     _check(st, "pa_evict")
 
 
@@ -462,13 +475,10 @@ def pa_cross_attention(out, q, k_cache, v_cache, block_tables, context_lens, q_s
     if workspace is None:
         need = pa_cross_attention_workspace_size(S, Hq, Hkv, D, B, Nq, int(max_query_len), int(max_context_len))
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    st = lib.pa_cross_attention(_dev_ptr(out, "out"), None if lse is None else _dev_ptr(lse, "lse"), _dev_ptr(q, "q"),
-                                _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"),
-                                _dev_ptr(block_tables, "block_tables"), _dev_ptr(context_lens, "context_lens"),
-                                _dev_ptr(q_start, "q_start"), S, Hq, Hkv, D, B, block_tables.shape[1], NB, Nq,
-                                int(max_query_len), int(max_context_len), float(scale),
-                                _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-                                _dtype_code(q), _stream(stream))
+    handle, (*ptrs, ws) = _launch(stream, out, lse, q, k_cache, v_cache, block_tables, context_lens, q_start, workspace)
+    st = lib.pa_cross_attention(*ptrs, S, Hq, Hkv, D, B, block_tables.shape[1], NB, Nq, int(max_query_len),
+                                int(max_context_len), float(scale), ws, workspace.numel() * workspace.element_size(),
+                                _dtype_code(q), handle)
     _check(st, "pa_cross_attention")
     return out
 
