@@ -605,11 +605,13 @@ static pa_status prefill_impl(const char* name, void* out, const void* q, const 
 
 namespace {
 
-// Layout of pa_cross_attention's workspace: entries and merge list, then the partial states.
+// Layout of pa_cross_attention's workspace: entries and merge list (or, with at most one query row per
+// sequence, the own tokens' entries and counters), then the partial states.
 struct CrossWorkspace {
     GroupWorkspace g;
-    size_t entries, merges, acc, ml, total;
+    size_t entries, merges, own, arrived, acc, ml, total;
     int chunks;
+    bool single;
 };
 
 CrossWorkspace cross_workspace(size_t S, size_t Hq, int Hkv, int D, size_t Nq, int max_query_len, int max_context_len)
@@ -617,6 +619,19 @@ CrossWorkspace cross_workspace(size_t S, size_t Hq, int Hkv, int D, size_t Nq, i
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     CrossWorkspace w{};
     const int G = (int)(Hq / (size_t)Hkv);
+    w.single = max_query_len <= 1;
+    if (w.single) {
+        w.chunks = shared_max_parts((int64_t)S, Hkv, max_context_len);
+        w.g = group_workspace(0, 0, 0);
+        w.own = w.g.end;
+        w.arrived = up(w.own + sizeof(OwnItem) * S * (size_t)w.chunks);
+        w.acc = up(w.arrived + 4 * Nq * (size_t)Hkv);
+        const size_t states = w.chunks > 1 ? Nq * Hq * (size_t)w.chunks : 0;
+        w.ml = up(w.acc + states * (size_t)D * 4);
+        w.total = up(w.ml + states * 8);
+        w.entries = S * (size_t)w.chunks;
+        return w;
+    }
     const size_t T = ((int64_t)max_query_len * G <= 64 ? 64 : 128) / (size_t)G;
     w.chunks = group_max_chunks(max_context_len, (int64_t)Nq, G, Hkv);
     w.entries = (S + Nq / T) * (size_t)w.chunks;
@@ -739,7 +754,22 @@ pa_status pa_cross_attention(void* out, float* lse, const void* q, const void* k
     a.max_query_len = max_query_len;
     a.max_context_len = max_context_len;
     a.max_chunks = w.chunks;
-    const cudaError_t e = launch_cross(a, head_dim, num_heads / num_kv_heads, static_cast<cudaStream_t>(stream));
+    cudaError_t e;
+    if (w.single) {
+        SharedArgs o{};
+        o.g = a.g;
+        o.context_lens = context_lens;
+        o.own = reinterpret_cast<OwnItem*>(ws + w.own);
+        o.arrived = reinterpret_cast<unsigned*>(ws + w.arrived);
+        o.num_seqs = num_seqs;
+        o.max_context_len = max_context_len;
+        o.max_parts = w.chunks;
+        o.g.lead_partitions = 0;
+        e = launch_cross_single(o, q_start, num_query_tokens, head_dim, num_heads / num_kv_heads,
+                                static_cast<cudaStream_t>(stream));
+    } else {
+        e = launch_cross(a, head_dim, num_heads / num_kv_heads, static_cast<cudaStream_t>(stream));
+    }
     if (e != cudaSuccess) return cuda_fail("pa_cross_attention launch", e);
     return PA_OK;
 }

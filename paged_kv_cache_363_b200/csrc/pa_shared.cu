@@ -32,9 +32,25 @@ constexpr int kPlanThreads = 1024;
 // Entry i, or one without tokens past the end.
 __device__ __forceinline__ OwnItem load_own(const OwnItem* items, unsigned i, unsigned n)
 {
-    if (i >= n) return OwnItem{0, 0, 0, 0, 0, 1, {0, 0}};
+    if (i >= n) return OwnItem{0, 0, 0, 0, 0, 1, 0, 0};
     const int4 x = __ldcg(reinterpret_cast<const int4*>(items + i)), y = __ldcg(reinterpret_cast<const int4*>(items + i) + 1);
-    return OwnItem{x.x, x.y, x.z, x.w, y.x, y.y, {0, 0}};
+    return OwnItem{x.x, x.y, x.z, x.w, y.x, y.y, y.z, 0};
+}
+
+// Half a warp's share of `tokens` own tokens, and the tokens of a row's parts (all the same but the last):
+// at least that share and 256 (joining a row's parts costs some 4 us), and no more parts than the row has
+// partial states for.
+__device__ __forceinline__ int own_share(unsigned tokens, int num_kv_heads, int own_warps)
+{
+    return (int)fminf((float)tokens * (float)num_kv_heads / (2.f * (float)own_warps), 1e9f);
+}
+__device__ __forceinline__ int own_part(int own, int share, int max_parts)
+{
+    const int p0 = max(share, 256);
+    if (own <= p0) return max(own, 1);
+    const int p = (max(p0, (own + max_parts - 1) / max_parts) + 15) / 16 * 16;
+    const int n = (own + p - 1) / p;
+    return n <= 1 ? own : ((own + n - 1) / n + 15) / 16 * 16;
 }
 
 // The plan, in one CTA.
@@ -43,8 +59,7 @@ __device__ __forceinline__ OwnItem load_own(const OwnItem* items, unsigned i, un
 //     shared: its rows attend to all their tokens on their own, which is the same result.
 //  2. Entries of the shared tokens: (tile of rows, chunk), a chunk's tiles next to each other.
 //  3. Entries of the own tokens: a row, or one of its parts, the longer half of the entries
-//     first.  A part is half a warp's share of all own tokens, at least 256 (joining a row's
-//     parts costs some 4 us) and as many as keep the row within its partial states.
+//     first.
 // A batch of up to 1024 rows keeps its per-row values in shared memory: the plan is on the
 // critical path, and most of it was trips to L2.
 __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const SharedArgs a, int T, int D, int group_ctas, int own_warps)
@@ -189,15 +204,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
     tok = __reduce_add_sync(0xffffffffu, tok);
     if (lane == 0 && tok) atomicAdd(&s_own, tok);
     __syncthreads();
-    const int share = (int)fminf((float)s_own * (float)a.g.num_kv_heads / (2.f * (float)own_warps), 1e9f);
-    // tokens of a row's parts, all the same but the last
-    auto part_of = [&](int own) {
-        const int p0 = max(share, 256);
-        if (own <= p0) return max(own, 1);
-        const int p = (max(p0, (own + a.max_parts - 1) / a.max_parts) + 15) / 16 * 16;
-        const int n = (own + p - 1) / p;
-        return n <= 1 ? own : ((own + n - 1) / n + 15) / 16 * 16;
-    };
+    const int share = own_share(s_own, a.g.num_kv_heads, own_warps);
+    auto part_of = [&](int own) { return own_part(own, share, a.max_parts); };
     const int big = max(32, share / 2);  // an entry of the first half
     unsigned nbig = 0;
     for (int s = tid; s < S; s += kPlanThreads) {
@@ -211,7 +219,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
         const int per = part_of(own), parts = own <= per ? 1 : (own + per - 1) / per;
         const unsigned i0 = per > big ? atomicAdd(&s_front, (unsigned)parts) : s_big + atomicAdd(&s_back, (unsigned)parts);
         for (int p = 0; p < parts; ++p)
-            a.own[i0 + p] = OwnItem{s, tok0 + p * per, min(per, own - p * per), lead, p, parts, {0, 0}};
+            a.own[i0 + p] = OwnItem{s, tok0 + p * per, min(per, own - p * per), lead, p, parts, s, 0};
         if (parts > 1)
             for (int h = 0; h < a.g.num_kv_heads; ++h) a.arrived[(size_t)s * a.g.num_kv_heads + h] = 0u;
     }
@@ -221,6 +229,62 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
         counts[0] = s_items;
         counts[2] = s_big + s_back;
     }
+}
+
+// The plan of single query rows (pa_cross_attention): an entry per sequence with a row, or per part of it.
+__global__ void __launch_bounds__(kPlanThreads, 1)
+    single_plan_kernel(const SharedArgs a, const int32_t* q_start, int num_query_tokens, int own_warps)
+{
+    __shared__ unsigned s_own, s_big, s_front, s_back;
+    pdl_launch_dependents();
+    const int tid = threadIdx.x, lane = tid & 31, S = a.num_seqs;
+    const int cap = min(a.max_context_len, (int)min((long long)a.g.max_blocks_per_seq * a.g.block_size, 0x7fffffffll));
+    if (tid == 0) s_own = s_big = s_front = s_back = 0;
+    // row and tokens of sequence s; no row where its data is bad
+    auto load = [&](int s, int& row, int& L, bool flag) {
+        const int q0 = __ldg(q_start + s), q1 = __ldg(q_start + s + 1);
+        L = __ldg(a.context_lens + s);
+        const bool bad = q0 < 0 || q1 > num_query_tokens || q1 < q0 || q1 - q0 > 1 || L < 0 || L > cap;
+        if (bad && flag) atomicOr(a.g.status, PA_DEV_BAD_CONTEXT);
+        row = bad || q1 == q0 ? -1 : q0;
+    };
+    int row0 = -1, L0 = 0;  // this thread's first sequence, loaded once
+    unsigned tok = 0;
+    for (int s = tid; s < S; s += kPlanThreads) {
+        int row, L;
+        load(s, row, L, true);
+        if (s == tid) {
+            row0 = row;
+            L0 = L;
+        }
+        if (row >= 0) tok += (unsigned)L;
+    }
+    tok = __reduce_add_sync(0xffffffffu, tok);
+    __syncthreads();
+    if (lane == 0 && tok) atomicAdd(&s_own, tok);
+    __syncthreads();
+    const int share = own_share(s_own, a.g.num_kv_heads, own_warps), big = max(32, share / 2);
+    unsigned nbig = 0;
+    for (int s = tid; s < S; s += kPlanThreads) {
+        int row = row0, L = L0;
+        if (s != tid) load(s, row, L, false);
+        const int per = own_part(L, share, a.max_parts);
+        if (row >= 0 && per > big) nbig += L <= per ? 1u : (unsigned)((L + per - 1) / per);
+    }
+    if (nbig) atomicAdd(&s_big, nbig);
+    __syncthreads();
+    for (int s = tid; s < S; s += kPlanThreads) {
+        int row = row0, L = L0;
+        if (s != tid) load(s, row, L, false);
+        if (row < 0) continue;
+        const int per = own_part(L, share, a.max_parts), parts = L <= per ? 1 : (L + per - 1) / per;
+        const unsigned i0 = per > big ? atomicAdd(&s_front, (unsigned)parts) : s_big + atomicAdd(&s_back, (unsigned)parts);
+        for (int p = 0; p < parts; ++p) a.own[i0 + p] = OwnItem{row, p * per, min(per, L - p * per), 0, p, parts, s, 0};
+        if (parts > 1)
+            for (int h = 0; h < a.g.num_kv_heads; ++h) a.arrived[(size_t)row * a.g.num_kv_heads + h] = 0u;
+    }
+    __syncthreads();
+    if (tid == 0) const_cast<unsigned*>(a.g.counts)[2] = s_big + s_back;
 }
 
 // The own tokens and the join.
@@ -482,6 +546,8 @@ __device__ __forceinline__ void write_row(const SharedArgs& a, size_t row0, OwnS
 {
     constexpr int NV = D / 64;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    if (a.g.lse && t == 0 && g < G)
+        a.g.lse[row0 + g] = st.l > 0.f ? (st.m + log2f(st.l)) * 0.6931471805599453f : -INFINITY;
     st.scale(st.l > 0.f ? 1.f / st.l : 0.f, t);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -515,7 +581,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2) shared_own_kernel(const __grid
     const int bshift = a.g.block_size == 16 ? 4 : 5;
     // The copying cursor: unit iu (kv head ikvh) at token itk, the block of that step, and the entry of the unit after.
     auto table_at = [&](const OwnItem& it, int tk) {
-        return it.ntok > 0 ? __ldg(a.g.block_tables + (size_t)it.row * a.g.max_blocks_per_seq + (tk >> bshift)) : 0;
+        return it.ntok > 0 ? __ldg(a.g.block_tables + (size_t)it.table_row * a.g.max_blocks_per_seq + (tk >> bshift)) : 0;
     };
     unsigned iu = first;
     OwnItem icur = load_own(a.own, iu / Hkv, iu < total ? entries : 0u);
@@ -672,6 +738,46 @@ cudaError_t launch_shared_d(const SharedArgs& a, int group, cudaStream_t stream)
 }
 
 }  // namespace
+
+namespace {
+
+template <int D, int G>
+cudaError_t launch_single_dg(const SharedArgs& a, const int32_t* q_start, int num_query_tokens, cudaStream_t stream)
+{
+    using C = OwnCfg<D, G>;
+    int dev = 0, sms = 148;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    cudaError_t e = cudaFuncSetAttribute(shared_own_kernel<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    SharedArgs args = a;
+    args.wait_first = 1;
+    const int64_t units = (int64_t)a.num_seqs * a.max_parts * a.g.num_kv_heads;
+    const unsigned grid = (unsigned)std::min<int64_t>((units + kOwnWarps - 1) / kOwnWarps, 2LL * sms);
+    single_plan_kernel<<<1, kPlanThreads, 0, stream>>>(args, q_start, num_query_tokens, 2 * sms * kOwnWarps);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    return launch_pdl(shared_own_kernel<D, G>, dim3(grid), dim3(kOwnThreads), (size_t)C::SMEM, stream, args);
+}
+
+template <int D>
+cudaError_t launch_single_d(const SharedArgs& a, const int32_t* q_start, int num_query_tokens, int group, cudaStream_t stream)
+{
+    switch (group) {
+        case 1: return launch_single_dg<D, 1>(a, q_start, num_query_tokens, stream);
+        case 2: return launch_single_dg<D, 2>(a, q_start, num_query_tokens, stream);
+        case 4: return launch_single_dg<D, 4>(a, q_start, num_query_tokens, stream);
+        case 8: return launch_single_dg<D, 8>(a, q_start, num_query_tokens, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_cross_single(const SharedArgs& a, const int32_t* q_start, int num_query_tokens, int head_dim, int group,
+                                cudaStream_t stream)
+{
+    return head_dim == 64 ? launch_single_d<64>(a, q_start, num_query_tokens, group, stream)
+                          : launch_single_d<128>(a, q_start, num_query_tokens, group, stream);
+}
 
 cudaError_t launch_shared(const SharedArgs& a, int head_dim, int group, cudaStream_t stream)
 {

@@ -8,13 +8,14 @@
 
 namespace pa {
 
-// Own tokens of one row: all of them, or one of several parts.
+// Own tokens of one query row: all of them, or one of several parts.
 struct OwnItem {
     int row;
     int tok0, ntok;
     int lead;         // partial states of the row's shared tokens
     int part, parts;
-    int pad[2];
+    int table_row;    // row of block_tables
+    int pad;
 };
 
 struct SharedArgs {
@@ -90,5 +91,10 @@ inline SharedWorkspace shared_workspace(size_t S, size_t Hq, int Hkv, int D, int
 }
 
 cudaError_t launch_shared(const SharedArgs& a, int head_dim, int group, cudaStream_t stream);
+
+// pa_cross_attention with at most one query row per sequence: the own tokens' kernel alone.  Of `a`: g (lse
+// too), context_lens, own, arrived, num_seqs, max_context_len, max_parts.
+cudaError_t launch_cross_single(const SharedArgs& a, const int32_t* q_start, int num_query_tokens, int head_dim, int group,
+                                cudaStream_t stream);
 
 }  // namespace pa

@@ -59,6 +59,41 @@ def test_cross_against_the_definition(pa, Hkv, G, D, B):
     _check(p, rows, q, out, lse, D ** -0.5, G)
 
 
+@pytest.mark.parametrize("Hkv,G,D,B", [(2, 1, 128, 16), (1, 2, 64, 32), (2, 4, 128, 32), (1, 8, 128, 16), (3, 1, 64, 16),
+                                       (2, 4, 64, 16), (1, 8, 64, 32)])
+def test_cross_single_rows(pa, Hkv, G, D, B):
+    """At most one query row per sequence, some without one and some without tokens, long ones in parts."""
+    lens = [1, 0, 15, 16, 17, 0, 64, 65, 300, 1029, 5000, 33, 5]
+    rows = [1, 1, 0, 1, 1, 0, 1, 1, 1, 1, 1, 0, 1]
+    p = Paged(lens, Hkv, B, D, torch.bfloat16, seed=Hkv + G * D + B)
+    q = p.q(sum(rows), Hkv * G)
+    for scale in (D ** -0.5, -0.3):
+        out, lse = _call(pa, p, rows, q, scale)
+        assert pa.pa_device_status() == 0
+        _check(p, rows, q, out, lse, scale, G)
+
+
+def test_cross_single_rows_many_and_bad(pa):
+    rng = np.random.default_rng(3)
+    S = 1500                                              # more sequences than plan threads
+    lens, rows = rng.integers(0, 300, S).tolist(), rng.integers(0, 2, S).tolist()
+    p = Paged(lens, 1, 16, 64, torch.bfloat16, seed=23)
+    q = p.q(sum(rows), 2)
+    out, lse = _call(pa, p, rows, q, 0.125)
+    assert pa.pa_device_status() == 0
+    _check(p, rows, q, out, lse, 0.125, 2)
+    k, v, tables, ctx = p.cuda()
+    start = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+    s = int(np.flatnonzero(np.array(rows) == 1)[7])
+    ctx[s] = 10 ** 6                                      # a context past its table
+    out2 = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    pa.pa_cross_attention(out2, q.cuda(), k, v, tables, ctx, torch.from_numpy(start).cuda(), 1, max(lens), 0.125)
+    torch.cuda.synchronize()
+    assert pa.pa_device_status() == pa.PA_DEV_BAD_CONTEXT
+    good = [i for i in range(len(q)) if i != start[s]]
+    assert torch.equal(out2[good], out[good]) and torch.all(out2[start[s]] == 7.0)
+
+
 @pytest.mark.parametrize("scale", [-0.2, 0.0, 2.0])
 def test_cross_scales(pa, scale):
     """A negative scale, none, and one that makes the softmax sharp (running maxima that grow far)."""
