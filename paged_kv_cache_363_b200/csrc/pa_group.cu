@@ -804,9 +804,16 @@ cudaError_t launch_group_d(const GroupArgs& a, int group, int tile_rows, int cta
 
 int group_resident_ctas(int sms) { return 2 * sms; }
 
-static bool cross_many_rows(int64_t rows, int64_t max_rows, int group, int num_kv_heads, int sms)
+// Many query rows: two query tiles of 128 rows per CTA share every K/V tile (pa_prefill.cu), where a sequence
+// fills them on average and there are enough of them to keep a third of the SMs busy.  Measured at head_dim
+// 128, tiles shared / this file's kernel, us:
+//   16 sequences of 1500 tokens, 32 query heads on 8: 64 rows 45.9 / 51, 128 rows 77.6 / 90
+//   4 sequences of 2000 tokens, 32 on 8: 64 rows (32 pairs of tiles) 50 / 43.8, 128 rows (64) 51.5 / 56.5
+//   64 sequences of 1500 tokens, 32 on 8: 32 rows (128 of a pair's 256) 115 / 95, 64 rows 141 / 146
+//   16 sequences of 1500 tokens, 16 on 16: 64 rows 66 / 49.7, 256 rows 79 / 91.5; 64 of 100 rows 203 / 160
+static bool cross_many_rows(int64_t rows, int64_t max_rows, int seqs, int group, int num_kv_heads, int sms)
 {
-    return max_rows * group >= 256 && rows * group / 256 * num_kv_heads >= sms;
+    return max_rows * group >= 256 && rows * group >= 192LL * seqs && rows * group / 256 * num_kv_heads >= sms / 3;
 }
 
 cudaError_t launch_group(const GroupArgs& a, int head_dim, int group, int tile_rows, int ctas, cudaStream_t stream)
@@ -826,9 +833,8 @@ cudaError_t launch_group_merge(const GroupArgs& a, int head_dim, cudaStream_t st
 cudaError_t launch_cross(const CrossArgs& a, int head_dim, int group, cudaStream_t stream)
 {
     const int sms = sm_count(), ctas = group_resident_ctas(sms);
-    // Many rows: two query tiles of 128 rows per CTA share every K/V tile (pa_prefill.cu), where there are
-    // enough of them to give every SM one whatever the sequences' tokens.  CROSSOVER
-    if (head_dim == 128 && cross_many_rows(a.num_query_tokens, a.max_query_len, group, a.g.num_kv_heads, sms)) {
+    if (head_dim == 128 &&
+        cross_many_rows(a.num_query_tokens, a.max_query_len, a.num_seqs, group, a.g.num_kv_heads, sms)) {
         PrefillArgs p{};
         p.out = a.g.out;
         p.q = a.g.q;

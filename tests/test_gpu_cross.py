@@ -142,6 +142,58 @@ def test_cross_many_rows(pa, Hkv, G, D):
     _check(p, rows, q, out, lse, D ** -0.5, G)
 
 
+# Enough rows that two tiles of 128 query rows share every K/V tile (head_dim 128).
+SHARED_TILES = [(2, 8, 16, [700, 0, 1, 129, 64, 257], [300, 70, 130, 0, 200, 150]),
+                (8, 1, 32, [1, 300, 63, 0, 31], [515, 257, 384, 260, 400]),
+                (4, 4, 16, [2000, 5, 0, 128], [129, 400, 33, 300]),
+                (8, 2, 16, [65, 17, 0, 511], [300, 200, 1, 399])]
+
+
+@pytest.mark.parametrize("Hkv,G,B,lens,rows", SHARED_TILES)
+@pytest.mark.parametrize("scale", [128 ** -0.5, -0.1, 0.0])
+def test_cross_rows_that_share_tiles(pa, Hkv, G, B, lens, rows, scale):
+    p = Paged(lens, Hkv, B, 128, torch.bfloat16, seed=31 + G)
+    q = p.q(sum(rows), Hkv * G)
+    out, lse = _call(pa, p, rows, q, scale)
+    assert pa.pa_device_status() == 0
+    _check(p, rows, q, out, lse, scale, G)
+
+
+def test_cross_rows_that_share_tiles_skip_bad_sequences_and_replay(pa):
+    Hkv, G, B, lens, rows = SHARED_TILES[2]
+    p = Paged(lens, Hkv, B, 128, torch.bfloat16, seed=33)
+    q = p.q(sum(rows), Hkv * G)
+    good, _ = _call(pa, p, rows, q, 0.1)
+    k, v, tables, ctx = p.cuda()
+    qd, start = q.cuda(), torch.from_numpy(np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)).cuda()
+    nbytes = pa.pa_cross_attention_workspace_size(4, Hkv * G, Hkv, 128, B, sum(rows), max(rows), 2000)
+    ws = torch.full((nbytes,), 255, dtype=torch.uint8, device="cuda")
+    side, outs, graphs = torch.cuda.Stream(), [torch.empty_like(qd) for _ in range(2)], []
+    side.wait_stream(torch.cuda.current_stream())
+    for o in outs:                                        # two graphs that share a workspace, replayed in turn
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            pa.pa_cross_attention(o, qd, k, v, tables, ctx, start, max(rows), 2000, 0.1, workspace=ws, stream=side)
+        graphs.append(g)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    assert pa.pa_device_status() == 0
+    assert all(torch.equal(o, good) for o in outs)
+    a = np.concatenate([[0], np.cumsum(rows)])
+    for s, L in ((0, 10 ** 6), (1, -3), (3, 129 + 10 ** 5)):
+        c = ctx.clone()
+        c[s] = L
+        out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+        pa.pa_cross_attention(out, qd, k, v, tables, c, start, max(rows), 2000, 0.1)
+        torch.cuda.synchronize()
+        assert pa.pa_device_status() == pa.PA_DEV_BAD_CONTEXT
+        assert torch.all(out[a[s]:a[s + 1]] == 7.0)
+        rest = [i for i in range(len(q)) if not a[s] <= i < a[s + 1]]
+        assert torch.equal(out[rest], good[rest])
+
+
 def test_cross_captured_on_another_stream_and_shared_workspace(pa):
     lens, rows = [333, 64, 2000], [3, 200, 1]
     p = Paged(lens, 2, 16, 128, torch.bfloat16, seed=14)
