@@ -40,9 +40,10 @@ __device__ __forceinline__ OwnItem load_own(const OwnItem* items, unsigned i, un
 // Half a warp's share of `tokens` own tokens, and the tokens of a row's parts (all the same but the last):
 // at least that share and 256 (joining a row's parts costs some 4 us), and no more parts than the row has
 // partial states for.
-__device__ __forceinline__ int own_share(unsigned tokens, int num_kv_heads, int own_warps)
+__device__ __forceinline__ int own_share(unsigned tokens, int rows, int num_kv_heads, int own_warps)
 {
-    return (int)fminf((float)tokens * (float)num_kv_heads / (2.f * (float)own_warps), 1e9f);
+    const float units = (float)rows * (float)num_kv_heads, warps = (float)own_warps;
+    return (int)fminf((float)tokens * (float)num_kv_heads / (3.f * units <= warps ? warps - 0.75f * units : 2.f * warps), 1e9f);
 }
 __device__ __forceinline__ int own_part(int own, int share, int max_parts)
 {
@@ -204,7 +205,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
     tok = __reduce_add_sync(0xffffffffu, tok);
     if (lane == 0 && tok) atomicAdd(&s_own, tok);
     __syncthreads();
-    const int share = own_share(s_own, a.g.num_kv_heads, own_warps);
+    const int share = own_share(s_own, S, a.g.num_kv_heads, own_warps);
     auto part_of = [&](int own) { return own_part(own, share, a.max_parts); };
     const int big = max(32, share / 2);  // an entry of the first half
     unsigned nbig = 0;
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     __syncthreads();
     if (lane == 0 && tok) atomicAdd(&s_own, tok);
     __syncthreads();
-    const int share = own_share(s_own, a.g.num_kv_heads, own_warps), big = max(32, share / 2);
+    const int share = own_share(s_own, S, a.g.num_kv_heads, own_warps), big = max(32, share / 2);
     unsigned nbig = 0;
     for (int s = tid; s < S; s += kPlanThreads) {
         int row = row0, L = L0;
@@ -309,16 +310,17 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
 // Lane (g, t) ends with dims 8g .. 8g+7 of each 64 of heads 2t and 2t + 1, and reads the other
 // states of the row the same way, 32 contiguous bytes each.
 constexpr int kOwnThreads = 128, kOwnWarps = 4, kStep = 16;
+constexpr int own_ctas(int head_dim) { return head_dim == 64 ? 4 : 2; }  // per SM
 
 template <int D, int G>
 struct OwnCfg {
     static constexpr int NH = D / 64;
     static constexpr int HALF = kStep * 128;               // 64 columns of a step's K or V
-    static constexpr int QBYTES = G * D * 2;
-    static constexpr int STAGE = 2 * NH * HALF + (QBYTES + 1023) / 1024 * 1024;
-    static constexpr int NST = (113 * 1024 - 512) / (kOwnWarps * STAGE);  // two CTAs per SM
+    static constexpr int CTAS = own_ctas(D);
+    static constexpr int STAGE = 2 * NH * HALF + (G * D * 2 + 127) / 128 * 128;
+    static constexpr int NST = (227 * 1024 / CTAS - 1024) / (kOwnWarps * STAGE);
     static constexpr int SMEM = kOwnWarps * NST * STAGE;
-    static_assert(NST >= 2 && 2 * (SMEM + 1024) <= 227 * 1024, "two CTAs per SM, two stages a warp");
+    static_assert(NST >= 2 && CTAS * (SMEM + 1024) <= 227 * 1024, "two stages a warp");
 };
 
 __device__ __forceinline__ uint32_t lo_pair(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x5410); }
@@ -566,7 +568,7 @@ __device__ __forceinline__ void write_row(const SharedArgs& a, size_t row0, OwnS
 }
 
 template <int D, int G>
-__global__ void __launch_bounds__(kOwnThreads, 2) shared_own_kernel(const __grid_constant__ SharedArgs a)
+__global__ void __launch_bounds__(kOwnThreads, own_ctas(D)) shared_own_kernel(const __grid_constant__ SharedArgs a)
 {
     using C = OwnCfg<D, G>;
     constexpr int NV = D / 64, NST = C::NST, CPR = D / 8;  // 16-byte chunks of a row
@@ -718,8 +720,8 @@ cudaError_t launch_shared_dg(const SharedArgs& a, cudaStream_t stream)
     SharedArgs args = a;
     args.wait_first = shares ? 0 : 1;
     const int64_t units = (int64_t)a.num_seqs * a.max_parts * a.g.num_kv_heads;
-    const unsigned grid = (unsigned)std::min<int64_t>((units + kOwnWarps - 1) / kOwnWarps, 2LL * sms);
-    shared_plan_kernel<<<1, kPlanThreads, 0, stream>>>(args, tile_rows / G, D, gctas, 2 * sms * kOwnWarps);
+    const unsigned grid = (unsigned)std::min<int64_t>((units + kOwnWarps - 1) / kOwnWarps, (int64_t)C::CTAS * sms);
+    shared_plan_kernel<<<1, kPlanThreads, 0, stream>>>(args, tile_rows / G, D, gctas, C::CTAS * sms * kOwnWarps);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (shares && (e = launch_group(args.g, D, G, tile_rows, gctas, stream)) != cudaSuccess) return e;
     return launch_pdl(shared_own_kernel<D, G>, dim3(grid), dim3(kOwnThreads), (size_t)C::SMEM, stream, args);
@@ -752,8 +754,8 @@ cudaError_t launch_single_dg(const SharedArgs& a, const int32_t* q_start, int nu
     SharedArgs args = a;
     args.wait_first = 1;
     const int64_t units = (int64_t)a.num_seqs * a.max_parts * a.g.num_kv_heads;
-    const unsigned grid = (unsigned)std::min<int64_t>((units + kOwnWarps - 1) / kOwnWarps, 2LL * sms);
-    single_plan_kernel<<<1, kPlanThreads, 0, stream>>>(args, q_start, num_query_tokens, 2 * sms * kOwnWarps);
+    const unsigned grid = (unsigned)std::min<int64_t>((units + kOwnWarps - 1) / kOwnWarps, (int64_t)C::CTAS * sms);
+    single_plan_kernel<<<1, kPlanThreads, 0, stream>>>(args, q_start, num_query_tokens, C::CTAS * sms * kOwnWarps);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     return launch_pdl(shared_own_kernel<D, G>, dim3(grid), dim3(kOwnThreads), (size_t)C::SMEM, stream, args);
 }
