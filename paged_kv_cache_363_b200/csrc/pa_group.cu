@@ -185,6 +185,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     pdl_wait_primary();       // the plan's entries are visible from here on
     pdl_launch_dependents();  // after it: a kernel that only needs the plan may start now
     const unsigned nunits = __ldcg(a.counts) * (unsigned)a.num_kv_heads;
+    // This CTA's k-th unit, there and back: entries come longest first, so each pair of rounds is the same for all.
+    auto unit_at = [&](unsigned k) {
+        return k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    };
 
     if (warp == kKWarp || warp == kVWarp) {
         const bool is_k = warp == kKWarp;
@@ -202,11 +206,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                        ? __ldg(a.block_tables + (size_t)it.table_row * a.max_blocks_per_seq + (it.kv0 + tok) / a.block_size)
                        : 0;
         };
-        unsigned u = blockIdx.x;
-        GroupItem it = load_item(a, u, nunits), nit = load_item(a, u + gridDim.x, nunits);
+        GroupItem it = load_item(a, unit_at(0), nunits), nit = load_item(a, unit_at(1), nunits);
         int next = lookup(it, 0);
-        for (; u < nunits && ok; u += gridDim.x) {
-            const GroupItem after = load_item(a, u + 2 * gridDim.x, nunits);
+        unsigned u;
+        for (unsigned k = 0; (u = unit_at(k)) < nunits && ok; ++k) {
+            const GroupItem after = load_item(a, unit_at(k + 2), nunits);
             const int kvh = (int)(u % (unsigned)a.num_kv_heads);
             const int n = (it.kvlen + kTok - 1) / kTok;
             if (n == 0) next = lookup(nit, 0);
@@ -284,14 +288,13 @@ __global__ void __launch_bounds__(kThreads, 2)
             bool ok = true;
             int t = 0;       // tiles whose P V was issued
             int done = 0;    // units with tokens finished
-            unsigned u = blockIdx.x;
             auto tiles_of = [&](unsigned unit) {
                 return unit < nunits ? (__ldcg(&a.items[unit / (unsigned)a.num_kv_heads].kvlen) + kTok - 1) / kTok : 0;
             };
-            int n = tiles_of(u), nn = tiles_of(u + gridDim.x);
+            int n = tiles_of(unit_at(0)), nn = tiles_of(unit_at(1));
             if (n > 0) ok = issue_qk(0, true);
-            for (; ok && u < nunits; u += gridDim.x) {
-                const int after = tiles_of(u + 2 * gridDim.x);
+            for (unsigned k = 0; ok && unit_at(k) < nunits; ++k) {
+                const int after = tiles_of(unit_at(k + 2));
                 for (int j = 0; j < n && ok; ++j, ++t) {
                     if (j + 1 < n && !(ok = issue_qk(t + 1, false))) break;
                     if (!mbar_wait_bounded(&p_full[t & 1], (t >> 1) & 1, abort_flag) ||
@@ -351,18 +354,18 @@ __global__ void __launch_bounds__(kThreads, 2)
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full);
         };
-        unsigned u = blockIdx.x;
-        GroupItem it = load_item(a, u, nunits), nit = load_item(a, u + gridDim.x, nunits);
+        GroupItem it = load_item(a, unit_at(0), nunits), nit = load_item(a, unit_at(1), nunits);
         int row = query_row(it);
         if (it.kvlen > 0) {
-            fetch_q(it, row, (int)(u % (unsigned)a.num_kv_heads));
+            fetch_q(it, row, (int)(unit_at(0) % (unsigned)a.num_kv_heads));
             q_ready();
         }
-        for (; u < nunits; u += gridDim.x) {
-            const GroupItem after = load_item(a, u + 2 * gridDim.x, nunits);
+        unsigned u;
+        for (unsigned k = 0; (u = unit_at(k)) < nunits; ++k) {
+            const GroupItem after = load_item(a, unit_at(k + 2), nunits);
             const int nrow = query_row(nit);
             const int kvh = (int)(u % (unsigned)a.num_kv_heads);
-            const int nkvh = (int)((u + gridDim.x) % (unsigned)a.num_kv_heads);
+            const int nkvh = (int)(unit_at(k + 1) % (unsigned)a.num_kv_heads);
             const int n = (it.kvlen + kTok - 1) / kTok;
             const bool valid = member < it.members;
             const bool active = (warp * 32) / G < it.members;  // the warp has a valid row
@@ -856,6 +859,7 @@ cudaError_t launch_cross(const CrossArgs& a, int head_dim, int group, cudaStream
         p.scale_log2 = a.g.scale_log2;
         p.lse = a.g.lse;
         p.max_context_len = a.max_context_len;
+        p.order = reinterpret_cast<int*>(const_cast<GroupItem*>(a.g.items));  // (as many entries as sequences at least)
         return launch_cross_rows(p, group, a.num_query_tokens, a.max_query_len, stream);
     }
     const int tile_rows = (int64_t)a.max_query_len * group <= 64 ? 64 : 128;

@@ -213,6 +213,7 @@ struct PrefillArgs {
     float scale_log2;
     float* lse;                // pa_cross_attention: [rows][num_heads] or null
     int max_context_len;       // pa_cross_attention: bound of context_lens
+    int* order;                // pa_cross_attention: [num_seqs] sequences, longest contexts first
 };
 
 cudaError_t launch_prefill(const PrefillArgs& a, int group, int num_query_tokens, int max_query_len,

@@ -543,6 +543,54 @@ __device__ __forceinline__ void absorb_states(const SharedArgs& a, size_t row0, 
     st.l += (g & 1) ? s1 : s0;
 }
 
+// A warp's state of a unit to and from its partial state `slot`.
+template <int D, int G>
+__device__ __forceinline__ void store_state(const SharedArgs& a, size_t row0, int slot, const OwnState<D>& st)
+{
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, np = a.g.num_partitions;
+    if (t == 0 && g < G) *reinterpret_cast<float2*>(a.g.ws_ml + ((row0 + g) * np + slot) * 2) = make_float2(st.m, st.l);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        if (2 * t + h < G) {
+            float4* acc = reinterpret_cast<float4*>(a.g.ws_acc + ((row0 + 2 * t + h) * np + slot) * D + 8 * g);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+                acc[c * 16] = make_float4(st.o[c * 4][h], st.o[c * 4 + 1][h], st.o[c * 4 + 2][h], st.o[c * 4 + 3][h]);
+                acc[c * 16 + 1] =
+                    make_float4(st.o[c * 4][h + 2], st.o[c * 4 + 1][h + 2], st.o[c * 4 + 2][h + 2], st.o[c * 4 + 3][h + 2]);
+            }
+        }
+}
+
+template <int D, int G>
+__device__ __forceinline__ void load_state(const SharedArgs& a, size_t row0, int slot, OwnState<D>& st)
+{
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, np = a.g.num_partitions;
+    st.clear();
+    if (g < G) {
+        const float2 v = __ldcg(reinterpret_cast<const float2*>(a.g.ws_ml) + (row0 + g) * np + slot);
+        st.m = v.x;
+        st.l = v.y;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        if (2 * t + h < G) {
+            const float4* acc = reinterpret_cast<const float4*>(a.g.ws_acc + ((row0 + 2 * t + h) * np + slot) * D + 8 * g);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+                const float4 lo = __ldcg(acc + c * 16), hi = __ldcg(acc + c * 16 + 1);
+                st.o[c * 4][h] = lo.x;
+                st.o[c * 4 + 1][h] = lo.y;
+                st.o[c * 4 + 2][h] = lo.z;
+                st.o[c * 4 + 3][h] = lo.w;
+                st.o[c * 4][h + 2] = hi.x;
+                st.o[c * 4 + 1][h + 2] = hi.y;
+                st.o[c * 4 + 2][h + 2] = hi.z;
+                st.o[c * 4 + 3][h + 2] = hi.w;
+            }
+        }
+}
+
 template <int D, int G>
 __device__ __forceinline__ void write_row(const SharedArgs& a, size_t row0, OwnState<D>& st)
 {
@@ -571,9 +619,9 @@ template <int D, int G>
 __global__ void __launch_bounds__(kOwnThreads, own_ctas(D)) shared_own_kernel(const __grid_constant__ SharedArgs a)
 {
     using C = OwnCfg<D, G>;
-    constexpr int NV = D / 64, NST = C::NST, CPR = D / 8;  // 16-byte chunks of a row
+    constexpr int NST = C::NST, CPR = D / 8;  // 16-byte chunks of a row
     extern __shared__ __align__(1024) unsigned char smem[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned Hkv = (unsigned)a.g.num_kv_heads;
     const uint32_t ring = smem_u32(smem) + warp * NST * C::STAGE;
     if (a.wait_first) pdl_wait_primary();
@@ -640,66 +688,74 @@ __global__ void __launch_bounds__(kOwnThreads, own_ctas(D)) shared_own_kernel(co
     for (int i = 0; i < NST; ++i) issue();
 
     bool waited = a.wait_first != 0;
+    // A unit whose row has shared tokens is joined with their states, which come late: the join is put off until this
+    // warp has nothing else to do (its last unit's state stays in registers), and `back` is the trip over those.
+    bool put_off = false, back = false;
     int sg = 0;  // stage of the next step
     OwnState<D> st;
     OwnItem it = load_own(a.own, first / Hkv, first < total ? entries : 0u);
-    for (unsigned u = first; u < total; u += hop) {
-        const OwnItem next = load_own(a.own, (u + hop) / Hkv, u + hop < total ? entries : 0u);
-        const int kvh = (int)(u % Hkv);
+    for (unsigned u = first; u < total;) {
+        const bool final = u + hop >= total;
+        const unsigned un = final ? first : u + hop;
+        const OwnItem next = load_own(a.own, un / Hkv, entries);
+        const unsigned kvh = u % Hkv;
         const size_t row0 = (size_t)it.row * a.g.num_heads + (size_t)kvh * G;
-        st.clear();
-        uint4 q[D / 32];
-        const int n = max(1, (it.ntok + kStep - 1) / kStep);
-        for (int j = 0; j < n; ++j) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(NST - 1) : "memory");
-            __syncwarp();
-            const uint32_t base = ring + sg * C::STAGE;
-            if (it.ntok > 0) {
-                if (j == 0) load_q<D, G>(base + 2 * C::NH * C::HALF, q);
-                own_step<D, G>(base, base + C::NH * C::HALF, it.ntok - j * kStep, a.g.scale_log2, q, st);
-            }
-            __syncwarp();  // every lane has read the stage
-            sg = sg + 1 == NST ? 0 : sg + 1;
-            issue();
-        }
-        st.l += __shfl_xor_sync(0xffffffffu, st.l, 1);
-        st.l += __shfl_xor_sync(0xffffffffu, st.l, 2);
-        bool last = true;
-        if (it.parts > 1) {
-            // this part's state; the last part of the row and kv head to get here joins them all, in order
-            const int np = a.g.num_partitions, sl = a.g.lead_partitions + it.part;
-            if (t == 0 && g < G)
-                *reinterpret_cast<float2*>(a.g.ws_ml + ((row0 + g) * np + sl) * 2) = make_float2(st.m, st.l);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                if (2 * t + h < G) {
-                    float4* acc = reinterpret_cast<float4*>(a.g.ws_acc + ((row0 + 2 * t + h) * np + sl) * D + 8 * g);
-#pragma unroll
-                    for (int c = 0; c < NV; ++c) {
-                        acc[c * 16] = make_float4(st.o[c * 4][h], st.o[c * 4 + 1][h], st.o[c * 4 + 2][h], st.o[c * 4 + 3][h]);
-                        acc[c * 16 + 1] =
-                            make_float4(st.o[c * 4][h + 2], st.o[c * 4 + 1][h + 2], st.o[c * 4 + 2][h + 2], st.o[c * 4 + 3][h + 2]);
-                    }
+        bool later;
+        if (!back) {
+            st.clear();
+            uint4 q[D / 32];
+            const int n = max(1, (it.ntok + kStep - 1) / kStep);
+            for (int j = 0; j < n; ++j) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(NST - 1) : "memory");
+                __syncwarp();
+                const uint32_t base = ring + sg * C::STAGE;
+                if (it.ntok > 0) {
+                    if (j == 0) load_q<D, G>(base + 2 * C::NH * C::HALF, q);
+                    own_step<D, G>(base, base + C::NH * C::HALF, it.ntok - j * kStep, a.g.scale_log2, q, st);
                 }
-            __threadfence();
-            __syncwarp();
-            unsigned before = 0;
-            if (lane == 0) before = atomicAdd(a.arrived + (size_t)it.row * Hkv + kvh, 1u);
-            before = __shfl_sync(0xffffffffu, before, 0);
-            __threadfence();
-            last = before == (unsigned)it.parts - 1;
-            if (last) st.clear();
+                __syncwarp();  // every lane has read the stage
+                sg = sg + 1 == NST ? 0 : sg + 1;
+                issue();
+            }
+            st.l += __shfl_xor_sync(0xffffffffu, st.l, 1);
+            st.l += __shfl_xor_sync(0xffffffffu, st.l, 2);
+            later = it.lead > 0 && !waited && !final;
+            put_off |= later;
+            if (it.parts > 1 || later) store_state<D, G>(a, row0, a.g.lead_partitions + it.part, st);
+        } else {
+            later = it.lead == 0 || final;  // (joined already)
+            if (!later && it.parts == 1) load_state<D, G>(a, row0, a.g.lead_partitions, st);
         }
-        if (last) {
+        if (!later) {
             if (it.lead > 0 && !waited) {
-                pdl_wait_primary();  // the shared tokens' states
+                pdl_wait_primary();
                 waited = true;
             }
-            const int lead = it.lead, skip = a.g.lead_partitions - lead;
-            absorb_states<D, G>(a, row0, st, lead + (it.parts > 1 ? it.parts : 0), 0, 1,
-                                [lead, skip](int p) { return p < lead ? p : p + skip; });
-            write_row<D, G>(a, row0, st);
+            // of several parts the last one here joins them all, in order
+            bool last = true;
+            if (it.parts > 1) {
+                __threadfence();
+                __syncwarp();
+                unsigned before = 0;
+                if (lane == 0) before = atomicAdd(a.arrived + (size_t)it.row * Hkv + kvh, 1u);
+                before = __shfl_sync(0xffffffffu, before, 0);
+                __threadfence();
+                last = before == (unsigned)it.parts - 1;
+                if (last) st.clear();
+            }
+            if (last) {
+                const int lead = it.lead, skip = a.g.lead_partitions - lead;
+                absorb_states<D, G>(a, row0, st, lead + (it.parts > 1 ? it.parts : 0), 0, 1,
+                                    [lead, skip](int p) { return p < lead ? p : p + skip; });
+                write_row<D, G>(a, row0, st);
+            }
         }
+        if (final) {
+            if (back || !put_off) break;
+            back = true;
+            __syncwarp();  // the states of this warp, read by other lanes than wrote them
+        }
+        u = un;
         it = next;
     }
     // whatever waits for this grid may count on the shared tokens' kernel having finished too
