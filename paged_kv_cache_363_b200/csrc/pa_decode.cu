@@ -109,7 +109,22 @@ cudaError_t encode_pool_map(CUtensorMap* out, const void* pool, uint64_t rows, i
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// The same from a small cache, which avoids re-encoding the maps of the same pools on every call.
+cudaError_t encode_pool_atoms(CUtensorMap* out, const void* pool, uint64_t rows, int D, int box_rows)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    if (!fn) return cudaErrorNotSupported;
+    std::memset(out, 0, sizeof(*out));
+    const cuuint64_t dims[4] = {64, 8, (cuuint64_t)D / 64, (cuuint64_t)rows / 8};
+    const cuuint64_t strides[3] = {(cuuint64_t)D * 2, 128, (cuuint64_t)D * 16};
+    const cuuint32_t box[4] = {64, 8, (cuuint32_t)D / 64, (cuuint32_t)box_rows / 8};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    const CUresult r = fn(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(pool), dims, strides, box,
+                          estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// encode_pool_map's maps from a small cache, which avoids re-encoding the maps of the same pools on every call.
 cudaError_t tensor_map(CUtensorMap* out, const void* pool, uint64_t rows, int D, int B)
 {
     struct Entry {

@@ -47,8 +47,7 @@ namespace {
 
 constexpr int kRows = 128;      // rows of an MMA tile
 constexpr int kTok = 64;        // tokens per K/V tile
-constexpr int kBox = 16;        // rows per TMA box
-constexpr int kNBox = kTok / kBox;
+constexpr int kNBox = kTok / 16;  // blocks per K/V tile, at most (a TMA box is a block's rows)
 constexpr int kThreads = 224;   // 4 softmax warps, producers of K and of V, MMA issuer
 constexpr int kKWarp = 4, kVWarp = 5, kMmaWarp = 6;
 constexpr uint32_t kTmemCols = 256;  // S 0..63 and 64..127 (P over their first 32), O 128..
@@ -61,8 +60,8 @@ template <int D, int QR>
 struct Cfg {
     static constexpr int NH = D / 64;             // 64-column halves
     static constexpr int QHALF = QR * 128;        // bytes of a half of Q
-    static constexpr int KVHALF = kTok * 128;     // bytes of a half of a K or V tile
-    static constexpr int TILE = NH * KVHALF;
+    static constexpr int ATOM = 8 * 128;          // 8 rows of a half of K or V (the halves of 8 rows lie together)
+    static constexpr int TILE = NH * kTok * 128;
     static constexpr int ST = (D == 128 ? 1 : 2) * (QR == 64 ? 3 : 2);  // stages of K and of V
     static constexpr int OFF_K = NH * QHALF;
     static constexpr int OFF_V = OFF_K + ST * TILE;
@@ -197,13 +196,14 @@ __global__ void __launch_bounds__(kThreads, 2)
         const CUtensorMap* map = is_k ? &tmap_k : &tmap_v;
         const uint32_t ring = smem_u32(smem) + (is_k ? C::OFF_K : C::OFF_V);
         const uint64_t pol = policy_evict_normal();
+        const int B = a.block_size;
         bool ok = true;
         int t = 0;  // tiles issued
         // physical block of box `lane` of tile j of a unit
         auto lookup = [&](const GroupItem& it, int j) -> int {
-            const int tok = j * kTok + lane * kBox;
-            return lane < kNBox && tok < it.kvlen
-                       ? __ldg(a.block_tables + (size_t)it.table_row * a.max_blocks_per_seq + (it.kv0 + tok) / a.block_size)
+            const int tok = j * kTok + lane * B;
+            return lane < kTok / B && tok < it.kvlen
+                       ? __ldg(a.block_tables + (size_t)it.table_row * a.max_blocks_per_seq + (it.kv0 + tok) / B)
                        : 0;
         };
         GroupItem it = load_item(a, unit_at(0), nunits), nit = load_item(a, unit_at(1), nunits);
@@ -217,29 +217,25 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int j = 0; j < n; ++j, ++t) {
                 int phys = next;
                 next = j + 1 < n ? lookup(it, j + 1) : lookup(nit, 0);
-                const int nbox = min(kNBox, (it.kvlen - j * kTok + kBox - 1) / kBox);
+                const int nbox = min(kTok, it.kvlen - j * kTok + B - 1) / B;
                 if ((unsigned)phys >= (unsigned)a.num_blocks) {
                     atomicOr(a.status, PA_DEV_BAD_BLOCK);
                     phys = 0;
                 }
-                const int row = (phys * a.num_kv_heads + kvh) * a.block_size +
-                                (it.kv0 + j * kTok + lane * kBox) % a.block_size;
-                int rows[kNBox];
+                const int grp = (phys * a.num_kv_heads + kvh) * (B / 8);
+                int groups[kNBox];
 #pragma unroll
-                for (int b = 0; b < kNBox; ++b) rows[b] = __shfl_sync(0xffffffffu, row, b);
+                for (int b = 0; b < kNBox; ++b) groups[b] = __shfl_sync(0xffffffffu, grp, b);
                 const int st = t % ST;
                 // one thread issues the boxes (lanes of a warp that each issue one take turns, and take longer)
                 if (lane == 0) {
                     if (t >= ST && !mbar_wait_bounded(&empty[st], ((t / ST) & 1) ^ 1, abort_flag)) ok = false;
                     if (ok) {
-                        mbar_arrive_expect_tx(&full[st], (uint32_t)(nbox * kBox * 128 * NH));
+                        mbar_arrive_expect_tx(&full[st], (uint32_t)(nbox * B * 128 * NH));
 #pragma unroll
                         for (int b = 0; b < kNBox; ++b)
                             if (b < nbox)
-#pragma unroll
-                                for (int h = 0; h < NH; ++h)
-                                    tma_load_2d(ring + st * C::TILE + h * C::KVHALF + b * kBox * 128, map, h * 64, rows[b],
-                                                &full[st], pol);
+                                tma_load_4d(ring + st * C::TILE + b * B * 128 * NH, map, 0, 0, 0, groups[b], &full[st], pol);
                     }
                 }
                 ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
@@ -279,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 for (int k = 0; k < D / 16; ++k) {
                     const uint32_t kk = (k & 3) * 32;
                     umma_bf16_ss(tmem + (t & 1) * kTok, umma_desc_sw128(sq + (k >> 2) * C::QHALF + kk, 16, 1024),
-                                 umma_desc_sw128(kb + (k >> 2) * C::KVHALF + kk, 16, 1024), idesc_qk, k > 0 ? 1u : 0u);
+                                 umma_desc_sw128(kb + (k >> 2) * C::ATOM + kk, 16, NH * C::ATOM), idesc_qk, k > 0 ? 1u : 0u);
                 }
                 umma_commit(&s_full[t & 1]);
                 umma_commit(&k_empty[t % ST]);
@@ -307,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     const uint32_t vb = sv + (t % ST) * C::TILE, p = tmem + (t & 1) * kTok;
 #pragma unroll
                     for (int k = 0; k < kTok / 16; ++k)
-                        umma_bf16_ts(tmem + 128, p + k * 8, umma_desc_sw128(vb + k * 16 * 128, C::KVHALF, 1024), idesc_pv,
+                        umma_bf16_ts(tmem + 128, p + k * 8, umma_desc_sw128(vb + k * 2 * NH * C::ATOM, C::ATOM, NH * C::ATOM), idesc_pv,
                                      (j > 0 || k > 0) ? 1u : 0u);
                     umma_commit(o_done);
                     umma_commit(&v_empty[t % ST]);
@@ -474,8 +470,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                     for (int i = r; i < (kTok - left) * NH * 8; i += 128) {
                         const int vr = left + i / (NH * 8), h = (i >> 3) % NH;
-                        *reinterpret_cast<uint4*>(smem + C::OFF_V + (t % ST) * C::TILE + h * C::KVHALF + vr * 128 +
-                                                  (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4*>(smem + C::OFF_V + (t % ST) * C::TILE + ((vr >> 3) * NH + h) * C::ATOM +
+                                                  (vr & 7) * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
                     }
                     fence_async_smem();
                 }
@@ -774,9 +770,9 @@ cudaError_t launch_group_dgq(const GroupArgs& a, int ctas, cudaStream_t stream)
     using C = Cfg<D, QR>;
     CUtensorMap tk, tv;
     const uint64_t rows = (uint64_t)a.num_blocks * a.num_kv_heads * a.block_size;
-    cudaError_t e = encode_pool_map(&tk, a.k_cache, rows, D, kBox);
+    cudaError_t e = encode_pool_atoms(&tk, a.k_cache, rows, D, a.block_size);
     if (e != cudaSuccess) return e;
-    if ((e = encode_pool_map(&tv, a.v_cache, rows, D, kBox)) != cudaSuccess) return e;
+    if ((e = encode_pool_atoms(&tv, a.v_cache, rows, D, a.block_size)) != cudaSuccess) return e;
     if ((e = cudaFuncSetAttribute(group_attention_kernel<D, G, QR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   C::SMEM)) != cudaSuccess)
         return e;

@@ -105,6 +105,9 @@ bool decode_uses_tensor_cores(pa_dtype dtype, int head_dim, int group);
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 cudaError_t tensor_map(CUtensorMap* out, const void* pool, uint64_t rows, int D, int box_rows);
 cudaError_t encode_pool_map(CUtensorMap* out, const void* pool, uint64_t rows, int D, int box_rows);  // no cache
+// The same pool as rows / 8 groups of 8 rows x D / 64 halves of 64 columns, boxes of `box_rows` whole rows: a box
+// lands group by group, the 8 x 128 bytes (a swizzle atom) of one half behind those of the other.
+cudaError_t encode_pool_atoms(CUtensorMap* out, const void* pool, uint64_t rows, int D, int box_rows);
 
 // Process-unique id of the CUDA context current on this thread (cuCtxGetId), or 0
 // when none is current or the driver lacks the call.  Device addresses of the
