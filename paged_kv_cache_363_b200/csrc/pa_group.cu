@@ -622,7 +622,7 @@ constexpr int kPlanThreads = 1024;
 
 __global__ void __launch_bounds__(kPlanThreads, 1) cross_plan_kernel(const CrossArgs a, int T, int D, int ctas)
 {
-    __shared__ unsigned s_steps, s_rows, s_class[kLenClasses], s_merges, s_over;
+    __shared__ unsigned s_steps, s_tiles, s_rows, s_class[kLenClasses], s_merges, s_over;
     __shared__ int s_longest;
     __shared__ int s_q0[kPlanThreads], s_n[kPlanThreads], s_len[kPlanThreads];
     pdl_launch_dependents();
@@ -631,7 +631,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) cross_plan_kernel(const Cross
     const bool split = a.max_chunks > 1;
     if (tid < kLenClasses) s_class[tid] = 0;
     if (tid == 0) {
-        s_steps = s_rows = 0;
+        s_steps = s_tiles = s_rows = 0;
         s_merges = s_over = 0;
         s_longest = 0;
     }
@@ -653,10 +653,11 @@ __global__ void __launch_bounds__(kPlanThreads, 1) cross_plan_kernel(const Cross
         }
     };
     // (sums may wrap for absurd batches: the chunk length is then a poor one, and no more)
-    unsigned steps = 0, nrows = 0;
+    unsigned steps = 0, tiles = 0, nrows = 0;
     int longest = 0;
     each(true, [&](int rows, int L) {
         steps += (unsigned)((rows + T - 1) / T) * (unsigned)((L + kTok - 1) / kTok);
+        tiles += (unsigned)((rows + T - 1) / T);
         nrows += (unsigned)rows;
         longest = max(longest, L);
     });
@@ -665,15 +666,17 @@ __global__ void __launch_bounds__(kPlanThreads, 1) cross_plan_kernel(const Cross
     if (split) {
         longest = __reduce_max_sync(0xffffffffu, longest);
         steps = __reduce_add_sync(0xffffffffu, steps);
+        tiles = __reduce_add_sync(0xffffffffu, tiles);
         nrows = __reduce_add_sync(0xffffffffu, nrows);
         if (lane == 0 && nrows) {
             atomicAdd(&s_steps, steps);
+            atomicAdd(&s_tiles, tiles);
             atomicAdd(&s_rows, nrows);
             atomicMax(&s_longest, longest);
         }
         __syncthreads();
-        chunk = plan_chunk((float)s_steps * (float)a.g.num_kv_heads, ctas, s_longest, (float)s_rows * (float)a.g.num_heads,
-                           a.max_chunks, D, false);
+        chunk = plan_chunk((float)s_steps * (float)a.g.num_kv_heads, (float)s_tiles * (float)a.g.num_kv_heads, ctas, s_longest,
+                           (float)s_rows * (float)a.g.num_heads, a.max_chunks, D, false);
     }
     // tokens of a sequence's chunks, all the same but the last, and their number
     auto chunks_of = [&](int L, int& per) {

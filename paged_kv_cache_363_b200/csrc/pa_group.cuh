@@ -74,17 +74,28 @@ inline int group_max_chunks(int64_t max_len, int64_t rows, int group, int num_kv
 }
 
 #ifdef __CUDACC__
-// The chunk length of a plan.  Split or not, from four sums: `steps` (tiles of rows x tiles of 64 tokens x kv
-// heads), the longest table, and the (row, head) pairs.  Unsplit, the time is the longest table's or the mean
+// The chunk length of a plan.  Split or not, from a few sums: `tiles` (tiles of rows x kv heads), `steps` (those
+// x tiles of 64 tokens), the longest table, and the (row, head) pairs.  Unsplit, the time is the longest table's or the mean
 // load's, at about 1 us a step; split into the mean load of a CTA (256 tokens at least), that load's and the
 // partial states' (written and read at 5 TB/s), and 4 us where a split brings a merge with it.
+// A chunk is long enough for the units to fit whole rounds of the CTAs, where the tiles are few enough to tell (each
+// ends in a part of a chunk, taken as 3/4): two rounds, where the states are joined anyway, so that the two CTAs of
+// an SM even out better, else one.  Halves of the mean load alone gave 608 units of
+// 155 rows on three documents of 23,000 to 32,000 tokens (32 query heads on 8) for 296 CTAs: 145 us, 125 fitted.
 // (Splitting every batch into two units per CTA cost 16 sequences x 64 rows x 1500 tokens 90 us, 60 unsplit.)
-__device__ __forceinline__ int plan_chunk(float steps, int ctas, int longest, float pairs, int max_chunks, int D, bool merge_anyway)
+__device__ __forceinline__ int plan_chunk(float steps, float tiles, int ctas, int longest, float pairs, int max_chunks, int D, bool merge_anyway)
 {
     const float load = steps / (float)ctas;
     const int least = (longest + max_chunks - 1) / max_chunks;
-    // (half of the mean where the states are joined anyway: the two CTAs of an SM even out better)
-    const int c = (max(max((int)fminf((merge_anyway ? 32.f : 64.f) * load, 1e9f), least), 256) + 63) / 64 * 64;
+    float fit = (merge_anyway ? 32.f : 64.f) * load;
+    for (int rounds = merge_anyway ? 2 : 1; rounds > 0; --rounds) {
+        const float units = (float)(rounds * ctas) - 0.75f * tiles;
+        if (units >= 0.5f * (float)(rounds * ctas)) {
+            fit = 64.f * steps / units;
+            if (fit >= 256.f) break;
+        }
+    }
+    const int c = (max(max((int)fminf(fit, 1e9f), least), 256) + 63) / 64 * 64;
     if (c >= longest) return max(longest, 1);
     const float whole = fmaxf((float)longest * (1.f / 64.f), load);
     const float states = pairs * ceilf((float)longest / (float)c);

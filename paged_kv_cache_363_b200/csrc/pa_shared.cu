@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
 {
     __shared__ int s_listed[kPlanThreads], s_ctx[kPlanThreads], s_lead[kPlanThreads], s_states[kPlanThreads];
     __shared__ int s_rows[kPlanThreads], s_start[kPlanThreads + 1], s_len[kPlanThreads], s_ok[kPlanThreads];
-    __shared__ unsigned s_steps, s_members, s_own, s_class[kLenClasses];
+    __shared__ unsigned s_steps, s_tiles, s_members, s_own, s_class[kLenClasses];
     __shared__ unsigned s_items, s_big, s_front, s_back;
     __shared__ int s_bad, s_longest;
     pdl_launch_dependents();
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
     const int* start = small ? s_start : a.group_start;
     const int* lens = small ? s_len : a.shared_lens;
     if (tid == 0) {
-        s_steps = s_members = s_own = 0;
+        s_steps = s_tiles = s_members = s_own = 0;
         s_items = s_big = s_front = s_back = 0;
         s_bad = s_longest = 0;
     }
@@ -136,7 +136,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
             group_ok[g] = ok && n > 0 && r1 > r0;
             if (!ok) atomicOr(a.g.status, PA_DEV_BAD_CONTEXT);
             else if (n > 0) {
-                atomicAdd(&s_steps, (unsigned)((r1 - r0 + T - 1) / T) * (unsigned)((n + 63) / 64));
+                const unsigned tiles = (unsigned)((r1 - r0 + T - 1) / T);
+                atomicAdd(&s_tiles, tiles);
+                atomicAdd(&s_steps, tiles * (unsigned)((n + 63) / 64));
                 atomicAdd(&s_members, (unsigned)(r1 - r0));
                 atomicMax(&s_longest, n);
             }
@@ -144,8 +146,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
     }
     __syncthreads();
     if (s_steps > 0) {
-        const int chunk = plan_chunk((float)s_steps * (float)a.g.num_kv_heads, group_ctas, s_longest,
-                                     (float)s_members * (float)a.g.num_heads, a.max_chunks, D, true);
+        const int chunk = plan_chunk((float)s_steps * (float)a.g.num_kv_heads, (float)s_tiles * (float)a.g.num_kv_heads,
+                                     group_ctas, s_longest, (float)s_members * (float)a.g.num_heads, a.max_chunks, D, true);
         auto chunks_of = [&](int n, int& per) {
             const int want = (n + chunk - 1) / chunk;
             per = ((n + want - 1) / want + 63) / 64 * 64;
