@@ -318,12 +318,17 @@ pa_status pa_decode_scores(void* out, float* scores, const void* q, const void* 
 }
 
 static size_t evict_counts_bytes(size_t rows) { return (rows * sizeof(unsigned) + 255) / 256 * 256; }
+static size_t evict_list_bytes(size_t rows, int max_context_len)
+{
+    return rows * sizeof(unsigned) * (size_t)std::max(1, max_context_len / 2);
+}
 
 size_t pa_evict_workspace_size(int num_seqs, int num_kv_heads, int max_context_len)
 {
     if (num_seqs <= 0 || num_kv_heads <= 0 || max_context_len < 0 || max_context_len > kMaxEvictContext) return 0;
     const size_t rows = (size_t)num_seqs * num_kv_heads;
-    return evict_counts_bytes(rows) + rows * sizeof(uint2) * (size_t)std::max(1, max_context_len / 2);
+    return evict_counts_bytes(rows) + 2 * evict_list_bytes(rows, max_context_len) +
+           rows * sizeof(uint32_t) * (size_t)((max_context_len + 31) / 32);
 }
 
 pa_status pa_evict(void* k_cache, void* v_cache, float* new_scores, int32_t* new_positions, const float* scores,
@@ -377,8 +382,11 @@ pa_status pa_evict(void* k_cache, void* v_cache, float* new_scores, int32_t* new
     a.context_lens = context_lens;
     a.keep_lens = keep_lens;
     a.counts = static_cast<unsigned*>(workspace);
-    a.moves = reinterpret_cast<uint2*>(static_cast<unsigned char*>(workspace) +
-                                       evict_counts_bytes((size_t)num_seqs * num_kv_heads));
+    unsigned char* lists = static_cast<unsigned char*>(workspace) + evict_counts_bytes((size_t)num_seqs * num_kv_heads);
+    const size_t list = evict_list_bytes((size_t)num_seqs * num_kv_heads, max_context_len);
+    a.dst = reinterpret_cast<unsigned*>(lists);
+    a.src = reinterpret_cast<unsigned*>(lists + list);
+    a.masks = reinterpret_cast<uint32_t*>(lists + 2 * list);
     a.status = status;
     a.num_recent = num_recent;
     a.num_seqs = num_seqs;

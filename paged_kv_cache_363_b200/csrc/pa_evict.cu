@@ -9,10 +9,15 @@
 // written instead of the whole kept context.  Sources (slots >= n) and destinations (slots
 // < n) are disjoint, so the moves run in any order.
 //
-// Two kernels.  evict_select (one CTA per (sequence, kv head)) finds the n-th largest key by
-// radix selection, 11 bits a pass, marks the kept tokens in a bit mask in shared memory, ranks
-// gaps and movers by prefix sums over the mask's words, and writes the move list and the new
-// scores and positions.  evict_move copies the K and V rows of the list.
+// Two kernels.  evict_select (one CTA per (sequence, kv head)) finds the n-th largest key,
+// marks the kept tokens in a bit mask in shared memory, ranks gaps and movers by prefix sums
+// over the mask's words, and writes the mask and the list of moves.  evict_move copies the K
+// and V rows of the list, and brings scores and positions along.
+//
+// The selection counts the keys in 2048 equal bins between the smallest and the largest (a
+// fixed split by leading bits would put most scores into a few bins, whose counters then take
+// them one by one), goes on in the bin of the n-th, and compares its last 256 or fewer keys
+// with one another: one or two passes, where fixed digits of 11 bits take three.
 // The selection is a chain of passes over the head's tokens, each a trip to memory long, and
 // there may be fewer heads than SMs: scores and positions are read once, eight loads in flight
 // per thread, and the keys stay in shared memory (contexts up to kCachedContext; longer ones
@@ -31,6 +36,7 @@ namespace {
 constexpr int kMoveThreads = 256;
 constexpr int kBins = 2048;
 constexpr int kCachedContext = 49152;  // keys (4 bytes) and two masks of a context in shared memory
+constexpr unsigned kFew = 256;         // keys of one bin that are compared with one another
 constexpr int kSmallContext = 4096;    // scores, positions, blocks and the move list as well
 
 // Where the head's tokens are kept while they are selected.
@@ -80,13 +86,15 @@ template <int THREADS, int WHERE, int CPR>
 __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictArgs a)
 {
     constexpr bool CACHED = WHERE != kFromGlobal, ALL = WHERE == kAllCached, MOVE = CPR > 0;
-    constexpr int UN = 8;                        // loads in flight per thread
-    constexpr int BPT = kBins / THREADS;         // bins per thread
-    extern __shared__ uint32_t s_mask[];         // kept tokens, then the ties: one bit each; then what is cached
+    constexpr int UN = THREADS == 1024 ? 16 : 8;  // loads in flight per thread
+    constexpr int UW = 4;                         // words of a warp at a time
+    constexpr int BPT = kBins / THREADS;          // bins per thread
+    extern __shared__ uint32_t s_mask[];          // kept tokens, then the ties: one bit each; then what is cached
     __shared__ unsigned s_hist[kBins];
     __shared__ unsigned long long s_warp[THREADS / 32];
-    __shared__ unsigned s_prefix, s_need;
+    __shared__ unsigned s_prefix, s_need, s_count, s_recent, s_few;
     __shared__ int s_max[THREADS / 32];
+    __shared__ unsigned s_lo[THREADS / 32], s_hi[THREADS / 32];
     const int sh = blockIdx.x;
     const int s = sh / a.num_kv_heads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -94,7 +102,7 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictArgs a
     if constexpr (!MOVE) pdl_launch_dependents();
     if (L < 0 || n < 0 || L > a.max_context_len || L > a.max_blocks_per_seq * a.block_size) {
         if (tid == 0) {
-            if constexpr (!MOVE) a.counts[sh] = 0;
+            if constexpr (!MOVE) a.counts[sh] = ~0u;
             if (sh % a.num_kv_heads == 0) atomicOr(a.status, PA_DEV_BAD_CONTEXT);
         }
         return;
@@ -111,7 +119,7 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictArgs a
             npos[i] = pos[i];
         }
         if constexpr (!MOVE)
-            if (tid == 0) a.counts[sh] = 0;
+            if (tid == 0) a.counts[sh] = ~0u;
         return;
     }
     const int words = (L + 31) / 32;
@@ -125,8 +133,9 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictArgs a
     uint16_t* s_mover = s_gap + L / 2;                            // [L / 2]
     if constexpr (MOVE)
         for (int i = tid; i < nblk; i += THREADS) s_blk[i] = __ldg(a.block_tables + (size_t)s * a.max_blocks_per_seq + i);
-    // keys, and the largest position
+    // keys and their range, and the largest position
     int mx = INT32_MIN;
+    uint32_t lo = 0xffffffffu, hi = 0u;
     for (int i0 = tid; i0 < L; i0 += THREADS * UN) {
         float x[UN];
         int p[UN];
@@ -134,26 +143,38 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictArgs a
         for (int k = 0; k < UN; ++k) {
             const int i = i0 + k * THREADS;
             p[k] = i < L ? pos[i] : INT32_MIN;
-            if constexpr (CACHED) x[k] = i < L ? sc[i] : 0.f;
+            x[k] = i < L ? sc[i] : 0.f;
         }
 #pragma unroll
         for (int k = 0; k < UN; ++k) {
             mx = max(mx, p[k]);
             const int i = i0 + k * THREADS;
-            if constexpr (CACHED)
-                if (i < L) s_key[i] = score_key(x[k]);
-            if constexpr (ALL)
-                if (i < L) {
+            if (i < L) {
+                const uint32_t y = score_key(x[k]);
+                lo = min(lo, y);
+                hi = max(hi, y);
+                if constexpr (CACHED) s_key[i] = y;
+                if constexpr (ALL) {
                     s_sc[i] = x[k];
                     s_pos[i] = p[k];
                 }
+            }
         }
     }
     mx = __reduce_max_sync(0xffffffffu, mx);
-    if (lane == 0) s_max[warp] = mx;
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0) {
+        s_max[warp] = mx;
+        s_lo[warp] = lo;
+        s_hi[warp] = hi;
+    }
+    if (tid == 0) s_recent = s_few = 0;
     for (int i = tid; i < kBins; i += THREADS) s_hist[i] = 0;
     __syncthreads();
     mx = __reduce_max_sync(0xffffffffu, lane < THREADS / 32 ? s_max[lane] : INT32_MIN);
+    lo = __reduce_min_sync(0xffffffffu, lane < THREADS / 32 ? s_lo[lane] : 0xffffffffu);
+    hi = __reduce_max_sync(0xffffffffu, lane < THREADS / 32 ? s_hi[lane] : 0u);
     // the recent tokens: positions within num_recent of the largest
     const int recent = min(a.num_recent, n);
     const long long fr = (long long)mx - recent + 1;
@@ -176,17 +197,30 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictArgs a
         if constexpr (CACHED) return s_key[i];
         return recent > 0 && pos[i] >= first_recent ? kRecentKey : score_key(sc[i]);
     };
-    // radix selection of the n-th largest key: bits 31-21, 20-10, 9-0
-    unsigned prefix = 0, need = (unsigned)n;
-    for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
-        const unsigned hi_mask = pass == 0 ? 0u : 0xffffffffu << (shift + (pass == 1 ? 11 : 10));
-        const unsigned bin_mask = pass == 2 ? 1023u : 2047u;
-        for (int i = tid; i < L; i += THREADS) {
-            const uint32_t k = key(i);
-            if ((k & hi_mask) == prefix) atomicAdd(&s_hist[(k >> shift) & bin_mask], 1u);
+    // the n-th largest key, `prefix`, and how many of its equals are among the n; the recent tokens lie above [lo, hi]
+    unsigned prefix = kRecentKey, need = (unsigned)n;
+    for (bool first = true;; first = false) {
+        const int shift = max(0, 21 - __clz((int)(hi - lo)));
+        unsigned seen = 0;  // recent tokens
+        for (int i0 = tid; i0 < L; i0 += THREADS * 8) {
+            uint32_t k[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) k[j] = i0 + j * THREADS < L ? key(i0 + j * THREADS) : 0u;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (i0 + j * THREADS < L && k[j] >= lo && k[j] <= hi) atomicAdd(&s_hist[(k[j] - lo) >> shift], 1u);
+                seen += k[j] == kRecentKey ? 1u : 0u;
+            }
+        }
+        if (first) {
+            seen = __reduce_add_sync(0xffffffffu, seen);
+            if (lane == 0 && seen) atomicAdd(&s_recent, seen);
         }
         __syncthreads();
+        if (first) {
+            if (s_recent >= need) break;
+            need -= s_recent;
+        }
         // thread t holds bins kBins - 1 - BPT * t and down
         unsigned c[BPT], sum = 0;
 #pragma unroll
@@ -198,12 +232,14 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictArgs a
         unsigned long long total;
         unsigned above = (unsigned)block_scan<THREADS>(sum, s_warp, &total);
         if (above < need && need <= above + sum) {
+            bool found = false;
 #pragma unroll
             for (int j = 0; j < BPT; ++j) {
-                if (above < need && need <= above + c[j]) {
-                    s_prefix = prefix | ((unsigned)(kBins - 1 - BPT * tid - j) << shift);
+                if (!found && need <= above + c[j]) {
+                    found = true;
+                    s_prefix = lo + ((unsigned)(kBins - 1 - BPT * tid - j) << shift);
                     s_need = need - above;
-                    need = 0;  // found
+                    s_count = c[j];
                 }
                 above += c[j];
             }
@@ -211,16 +247,56 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictArgs a
         __syncthreads();
         prefix = s_prefix;
         need = s_need;
+        const unsigned count = s_count;
+        if (shift == 0) break;
+        hi = min(hi, prefix + ((1u << shift) - 1u));
+        lo = prefix;
+        if (count > kFew) continue;
+        // few left: each is compared with all
+        for (int i0 = tid; i0 < L; i0 += THREADS * 8) {
+            uint32_t k[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) k[j] = i0 + j * THREADS < L ? key(i0 + j * THREADS) : kRecentKey;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (k[j] >= lo && k[j] <= hi) s_hist[atomicAdd(&s_few, 1u)] = k[j];
+        }
+        __syncthreads();
+        if (tid < count) {
+            const uint32_t mine = s_hist[tid];
+            unsigned more = 0, same = 0;
+            for (unsigned j = 0; j < count; ++j) {
+                const uint32_t k = s_hist[j];
+                more += k > mine ? 1u : 0u;
+                same += k == mine ? 1u : 0u;
+            }
+            if (more < need && need <= more + same) {  // (the same from every equal)
+                s_prefix = mine;
+                s_need = need - more;
+            }
+        }
+        __syncthreads();
+        prefix = s_prefix;
+        need = s_need;
+        break;
     }
     // masks of the keys above the threshold, and of those equal to it
-    for (int w = warp; w < words; w += THREADS / 32) {
-        const int i = w * 32 + lane;
-        const uint32_t k = i < L ? key(i) : 0u;
-        const uint32_t gt = __ballot_sync(0xffffffffu, i < L && k > prefix);
-        const uint32_t eq = __ballot_sync(0xffffffffu, i < L && k == prefix);
-        if (lane == 0) {
-            s_mask[w] = gt;
-            s_tie[w] = eq;
+    for (int wb = warp; wb < words; wb += THREADS / 32 * UW) {
+        uint32_t k[UW];
+#pragma unroll
+        for (int j = 0; j < UW; ++j) {
+            const int i = (wb + j * (THREADS / 32)) * 32 + lane;
+            k[j] = i < L ? key(i) : 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < UW; ++j) {
+            const int w = wb + j * (THREADS / 32), i = w * 32 + lane;
+            const uint32_t gt = __ballot_sync(0xffffffffu, i < L && k[j] > prefix);
+            const uint32_t eq = __ballot_sync(0xffffffffu, i < L && k[j] == prefix);
+            if (lane == 0 && w < words) {
+                s_mask[w] = gt;
+                s_tie[w] = eq;
+            }
         }
     }
     __syncthreads();
@@ -244,30 +320,53 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictArgs a
         const uint32_t front = below >= 32 ? 0xffffffffu : (below <= 0 ? 0u : (1u << below) - 1u);
         cnt += (unsigned long long)__popc(~kept & front) | (unsigned long long)__popc(kept & ~front) << 32;
     }
-    // gaps before slot n (low half) and kept tokens behind it (high half): as many of each
+    // gaps before slot n (low half) and kept tokens behind it (high half): as many of each.  A word has one kind or
+    // the other, but for the one that slot n is in, whose kept tokens are the first to move.
     rank = block_scan<THREADS>(cnt, s_warp, &total);
-    uint2* moves = a.moves + (size_t)sh * a.move_stride;
-    unsigned gap = (unsigned)rank, mover = (unsigned)(rank >> 32);
     for (int w = w0; w < w1; ++w) {
         const uint32_t kept = s_mask[w];
         const int below = n - w * 32;
         const uint32_t front = below >= 32 ? 0xffffffffu : (below <= 0 ? 0u : (1u << below) - 1u);
-        for (uint32_t b = ~kept & front; b; b &= b - 1) {
-            const int i = w * 32 + __ffs(b) - 1;
-            if constexpr (ALL) s_gap[gap] = (uint16_t)i;
-            if constexpr (!MOVE) moves[gap].x = (unsigned)i;
-            ++gap;
+        s_tie[w] = below > 0 ? (unsigned)rank : (unsigned)(rank >> 32);
+        rank += (unsigned long long)__popc(~kept & front) | (unsigned long long)__popc(kept & ~front) << 32;
+    }
+    __syncthreads();
+    const size_t list = (size_t)sh * a.move_stride;
+    for (int wb = warp; wb < words; wb += THREADS / 32 * UW) {
+        uint32_t kepts[UW], base[UW];
+#pragma unroll
+        for (int j = 0; j < UW; ++j) {
+            const int w = wb + j * (THREADS / 32);
+            kepts[j] = w < words ? s_mask[w] : 0u;
+            base[j] = w < words ? s_tie[w] : 0u;
         }
-        for (uint32_t b = kept & ~front; b; b &= b - 1) {
-            const int i = w * 32 + __ffs(b) - 1;
-            if constexpr (ALL) s_mover[mover] = (uint16_t)i;
-            if constexpr (!MOVE) moves[mover].y = (unsigned)i;
-            ++mover;
+#pragma unroll
+        for (int j = 0; j < UW; ++j) {
+            const int w = wb + j * (THREADS / 32), i = w * 32 + lane;
+            if (w >= words) break;
+            const uint32_t kept = kepts[j], lt = (1u << lane) - 1u;
+            const bool in = kept >> lane & 1u;
+            const int below = n - w * 32;
+            const uint32_t front = below >= 32 ? 0xffffffffu : (below <= 0 ? 0u : (1u << below) - 1u);
+            if (i < n) {
+                const unsigned r = base[j] + __popc(~kept & lt);
+                if (!in) {
+                    if constexpr (ALL) s_gap[r] = (uint16_t)i;
+                    if constexpr (!MOVE) a.dst[list + r] = (unsigned)i;
+                }
+            } else if (in) {
+                const unsigned r = (below > 0 ? 0u : base[j]) + __popc(kept & ~front & lt);
+                if constexpr (ALL) s_mover[r] = (uint16_t)i;
+                if constexpr (!MOVE) a.src[list + r] = (unsigned)i;
+            }
         }
     }
+    if constexpr (!ALL)
+        for (int w = tid; w < words; w += THREADS) a.masks[(size_t)sh * ((a.max_context_len + 31) / 32) + w] = s_mask[w];
     const unsigned count = (unsigned)total;
     if constexpr (!MOVE)
         if (tid == 0) a.counts[sh] = count;
+    if constexpr (!ALL) return;  // the moving kernel brings the scores and positions along
     __syncthreads();
     if constexpr (MOVE) {
         // the rows first: they are what takes the time
@@ -307,66 +406,83 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictArgs a
     }
     // the scores and positions of the slots before n (these arrays may be the old ones: a slot
     // before n is only ever written with its own value or one from behind n)
-    for (int i0 = tid; i0 < n; i0 += THREADS * UN) {
-        float x[UN];
-        int p[UN];
-#pragma unroll
-        for (int k = 0; k < UN; ++k) {
-            const int i = i0 + k * THREADS;
-            if (i < n) {
-                x[k] = ALL ? s_sc[i] : sc[i];
-                p[k] = ALL ? s_pos[i] : pos[i];
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < UN; ++k) {
-            const int i = i0 + k * THREADS;
-            if (i < n && (s_mask[i / 32] >> (i % 32) & 1u)) {
-                nsc[i] = x[k];
-                npos[i] = p[k];
-            }
-        }
-    }
     if constexpr (ALL) {
+        for (int i = tid; i < n; i += THREADS)
+            if (s_mask[i / 32] >> (i % 32) & 1u) {
+                nsc[i] = s_sc[i];
+                npos[i] = s_pos[i];
+            }
         for (unsigned r = tid; r < count; r += THREADS) {
             const int f = s_mover[r], d = s_gap[r];
             nsc[d] = s_sc[f];
             npos[d] = s_pos[f];
         }
-    } else {
-        for (unsigned r0 = tid; r0 < count; r0 += THREADS * 4) {
-            uint2 m[4];
-            float x[4];
-            int p[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (r0 + k * THREADS < count) m[k] = moves[r0 + k * THREADS];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (r0 + k * THREADS < count) {
-                    x[k] = sc[m[k].y];
-                    p[k] = pos[m[k].y];
-                }
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (r0 + k * THREADS < count) {
-                    nsc[m[k].x] = x[k];
-                    npos[m[k].x] = p[k];
-                }
-        }
     }
 }
 
-// CPR threads per row (16 bytes each), the K and the V row of a move together.
+// `splits` CTAs move each head's rows, CPR threads per row (16 bytes each), the K and the V row of a move together.
+// `carry` more CTAs before them (0: none) bring its scores and positions along, those of the slots before n, as above.
 template <int CPR>
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a, int splits)
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a, int carry, int splits)
 {
     pdl_wait_primary();
     constexpr int RPI = kMoveThreads / CPR;  // moves per step of the CTA
-    const int sh = blockIdx.x / splits, part = blockIdx.x % splits;
+    const int sh = blockIdx.x / (carry + splits), part = (int)(blockIdx.x % (carry + splits)) - carry;
     const int s = sh / a.num_kv_heads, kvh = sh % a.num_kv_heads;
-    const unsigned count = __ldg(a.counts + sh);
-    const uint2* moves = a.moves + (size_t)sh * a.move_stride;
+    const unsigned count = __ldcg(a.counts + sh);
+    if (count == ~0u) return;
+    const size_t list = (size_t)sh * a.move_stride;
+    if (part < 0) {
+        const size_t row = (size_t)sh * a.score_stride;
+        const uint32_t* mask = a.masks + (size_t)sh * ((a.max_context_len + 31) / 32);
+        const int n = min(__ldg(a.keep_lens + s), __ldg(a.context_lens + s)), hop = carry * kMoveThreads;
+        const int first = (part + carry) * kMoveThreads + threadIdx.x;
+        constexpr int UN = 4;
+        for (int r0 = first; r0 < (int)count; r0 += hop * UN) {
+            unsigned d[UN], f[UN];
+            float x[UN];
+            int p[UN];
+#pragma unroll
+            for (int k = 0; k < UN; ++k)
+                if (r0 + k * hop < (int)count) {
+                    d[k] = __ldcg(a.dst + list + r0 + k * hop);
+                    f[k] = __ldcg(a.src + list + r0 + k * hop);
+                }
+#pragma unroll
+            for (int k = 0; k < UN; ++k)
+                if (r0 + k * hop < (int)count) {
+                    x[k] = a.scores[row + f[k]];
+                    p[k] = a.positions[row + f[k]];
+                }
+#pragma unroll
+            for (int k = 0; k < UN; ++k)
+                if (r0 + k * hop < (int)count) {
+                    a.new_scores[row + d[k]] = x[k];
+                    a.new_positions[row + d[k]] = p[k];
+                }
+        }
+        for (int i0 = first; i0 < n; i0 += hop * UN) {
+            uint32_t m[UN];
+            float x[UN];
+            int p[UN];
+#pragma unroll
+            for (int k = 0; k < UN; ++k) {
+                const int i = i0 + k * hop;
+                m[k] = i < n ? __ldcg(mask + i / 32) : 0u;
+                x[k] = i < n ? a.scores[row + i] : 0.f;
+                p[k] = i < n ? a.positions[row + i] : 0;
+            }
+#pragma unroll
+            for (int k = 0; k < UN; ++k) {
+                const int i = i0 + k * hop;
+                if (i < n && (m[k] >> (i % 32) & 1u)) {
+                    a.new_scores[row + i] = x[k];
+                    a.new_positions[row + i] = p[k];
+                }
+            }
+        }
+        return;
+    }
     const int32_t* table = a.block_tables + (size_t)s * a.max_blocks_per_seq;
     const int c = threadIdx.x % CPR;
     uint4* kc = static_cast<uint4*>(a.k_cache);
@@ -381,9 +497,9 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
         return (((size_t)b * a.num_kv_heads + kvh) * a.block_size + tok % (unsigned)a.block_size) * CPR + c;
     };
     for (unsigned r = part * RPI + threadIdx.x / CPR; r < count; r += splits * RPI) {
-        const uint2 m = __ldg(moves + r);
+        const unsigned d = __ldcg(a.dst + list + r), f = __ldcg(a.src + list + r);
         bool ok = true;
-        const size_t dst = row_of(m.x, ok), src = row_of(m.y, ok);
+        const size_t dst = row_of(d, ok), src = row_of(f, ok);
         if (ok) {
             const uint4 kv = kc[src], vv = vc[src];
             kc[dst] = kv;
@@ -427,11 +543,12 @@ cudaError_t launch_evict(const EvictArgs& a, int head_dim, int elt_bytes, cudaSt
     int splits = (148 * 16 + rows - 1) / rows;
     splits = splits < steps ? splits : steps;
     splits = splits < 1 ? 1 : splits;
-    const dim3 grid((unsigned)rows * (unsigned)splits);
+    const int carry = small ? 0 : (a.max_context_len + 8191) / 8192;
+    const dim3 grid((unsigned)rows * (unsigned)(carry + splits));
     switch (cpr) {
-        case 8: return launch_pdl(evict_move_kernel<8>, grid, dim3(kMoveThreads), 0, stream, a, splits);
-        case 16: return launch_pdl(evict_move_kernel<16>, grid, dim3(kMoveThreads), 0, stream, a, splits);
-        case 32: return launch_pdl(evict_move_kernel<32>, grid, dim3(kMoveThreads), 0, stream, a, splits);
+        case 8: return launch_pdl(evict_move_kernel<8>, grid, dim3(kMoveThreads), 0, stream, a, carry, splits);
+        case 16: return launch_pdl(evict_move_kernel<16>, grid, dim3(kMoveThreads), 0, stream, a, carry, splits);
+        case 32: return launch_pdl(evict_move_kernel<32>, grid, dim3(kMoveThreads), 0, stream, a, carry, splits);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -151,8 +151,10 @@ struct EvictArgs {
     const int32_t* block_tables;
     const int32_t* context_lens;
     const int32_t* keep_lens;
-    unsigned* counts;          // [S * Hkv] moves of each (sequence, kv head)
-    uint2* moves;              // [S * Hkv][move_stride] (destination slot, source slot)
+    unsigned* counts;          // [S * Hkv] moves of each (sequence, kv head), or ~0: nothing to do at all
+    unsigned* dst;             // [S * Hkv][move_stride] destination slots
+    unsigned* src;             // [S * Hkv][move_stride] source slots
+    uint32_t* masks;           // [S * Hkv][(max_context_len + 31) / 32] kept tokens
     unsigned int* status;
     int num_recent;
     int num_seqs;
