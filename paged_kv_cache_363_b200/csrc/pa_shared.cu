@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
         }
     }
     __syncthreads();
-    if (s_steps > 0) {
+    if (s_steps > 0 && !a.wait_first) {
         const int chunk = plan_chunk((float)s_steps * (float)a.g.num_kv_heads, (float)s_tiles * (float)a.g.num_kv_heads,
                                      group_ctas, s_longest, (float)s_members * (float)a.g.num_heads, a.max_chunks, D, true);
         auto chunks_of = [&](int n, int& per) {
@@ -774,10 +774,15 @@ cudaError_t launch_shared_dg(const SharedArgs& a, cudaStream_t stream)
     if (e != cudaSuccess) return e;
     const int tile_rows = shared_tile_rows(a.num_groups, a.num_group_rows, G);
     const int gctas = group_resident_ctas(sms);
-    const bool shares = a.g.max_entries > 0;
+    const int64_t units = (int64_t)a.num_seqs * a.max_parts * a.g.num_kv_heads;
+    // Rows so short that their warps read them in twelve steps, and few enough for a warp per row and kv head: the
+    // shared tokens' kernel would take longer than reading them once per row.  Shared / not, graph replay, us: 4 rows x 8
+    // heads of 116 tokens 14.9 / 11.5 (head_dim 64), 16.4 / 13.4 (128), 212 tokens 15.3 / 14.6 and 16.8 / 17.4; 128 rows x
+    // 8 heads x 4 of 116 tokens 18.1 / 13.5 and 21.8 / 16.2, 212 tokens 18.7 / 17.4 and 22.0 / 21.8, 308 20.2 / 22.8 and 24.9 / 35.6.
+    const bool brief = a.max_context_len <= 192 && (int64_t)a.num_seqs * a.g.num_kv_heads <= (int64_t)C::CTAS * sms * kOwnWarps;
+    const bool shares = a.g.max_entries > 0 && !brief;
     SharedArgs args = a;
     args.wait_first = shares ? 0 : 1;
-    const int64_t units = (int64_t)a.num_seqs * a.max_parts * a.g.num_kv_heads;
     const unsigned grid = (unsigned)std::min<int64_t>((units + kOwnWarps - 1) / kOwnWarps, (int64_t)C::CTAS * sms);
     shared_plan_kernel<<<1, kPlanThreads, 0, stream>>>(args, tile_rows / G, D, gctas, C::CTAS * sms * kOwnWarps);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;

@@ -237,3 +237,33 @@ def test_batches_decode_shared(pa, wid, over):
         assert rows.numel() > 0 and longest > 0
     # each side is within a weight's rounding of the definition; values of V are below 6
     assert float((plain - shared).abs().max()) <= 6 * 2.0 ** -8 + 2 * 2.0 ** -8 * float(plain.abs().max())
+
+
+def test_shared_bad_group_beside_a_good_one(pa):
+    """Contexts long enough that the good group's tokens are read once for all its rows."""
+    p, q, groups = _batch(1, 2, 128, 16, seed=30, groups=[(4, 16, [1, 30]), (3, 14, [20])], singles=[300])
+    (r0, n0), (r1, n1) = groups
+    S = len(p.lens)
+    for rows, starts, lens in (
+            ([r0, r1], [0, 4, 7], [n0 + 1, n1]), ([r0, r1], [0, 4, 7], [n0, 16 * 50]), ([r0, r1], [0, 4, 7], [-16, n1]),
+            ([r0, [S, r1[1], r1[2]]], [0, 4, 7], [n0, n1]), ([r0, [r0[0], r1[1], r1[2]]], [0, 4, 7], [n0, n1]),
+            ([r0, r1], [0, 5, 4], [n0, n1])):
+        k, v, tables, ctx = p.cuda()
+        out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+        pa.pa_decode_shared(out, q.cuda(), k, v, tables, ctx, _i32(sum(rows, [])), _i32(starts), _i32(lens), max(p.lens),
+                            304, 0.1)
+        torch.cuda.synchronize()
+        assert pa.pa_device_status() == pa.PA_DEV_BAD_CONTEXT, (starts, lens)
+        _check(p, q, out, 0.1, 2)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("single", [1, 192, 193])
+def test_shared_brief_contexts(pa, D, single):
+    """Contexts of up to 192 tokens are read per row, longer ones once per group."""
+    p, q, groups = _batch(2, 4, D, 16, seed=31 + single, groups=[(4, 5, [1, 17, 40]), (9, 8, [0, 64]), (2, 12, [0])],
+                          singles=[single, 0])
+    assert max(p.lens) == max(single, 192)
+    out = _call(pa, p, q, groups, D ** -0.5)
+    assert pa.pa_device_status() == 0
+    _check(p, q, out, D ** -0.5, 4)
