@@ -13,9 +13,10 @@
 // padded by whatever the group lacks, which costs nothing: a 64-token tile of K and V (32 KB
 // at D = 128) takes 0.74 us at a 148th of the measured copy rate, its two products 0.27 us.
 //
-// A CTA runs units (entry, kv head) b, b + grid, ...; two CTAs per SM, each with
-//   - warps 4 and 5: K and V by TMA, one 16-row box per (16-token run of a block, 64
-//     columns), 128-byte swizzle, rings of ST stages that run on across units;
+// A CTA runs every grid-th unit (entry, kv head), there and back; two CTAs per SM, each with
+//   - warps 4 and 5: K and V by TMA, a block and kv head per box (a box per half of the
+//     columns took 1 to 2 us more of 70 to 97), 128-byte swizzle, rings of ST stages that run
+//     on across units;
 //   - warp 6 (one thread): S = Q K^T (M = 128, N = 64) into one of two tensor-memory buffers
 //     and O += P V (A = P from tensor memory, V MN-major); S of the next tile is issued before
 //     P V of this one, so the tensor core works while the softmax does;

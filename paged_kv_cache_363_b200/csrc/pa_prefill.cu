@@ -810,7 +810,7 @@ cudaError_t launch_group_of(const PrefillArgs& a, int group, int num_query_token
 }
 
 // A CTA per sequence: its place among them by context, longest first (16 sequences of 1000 to 3000 tokens:
-// 305 us as they come, ORDERED us so), and zero rows, -inf, where it has no tokens.  Also zeroes the item counter.
+// 305 us as they come, 296 us so), and zero rows, -inf, where it has no tokens.  Also zeroes the item counter.
 __global__ void __launch_bounds__(256) cross_order_kernel(const PrefillArgs a)
 {
     pdl_launch_dependents();
