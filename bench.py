@@ -70,8 +70,9 @@ def measured_hbm_peak():
         return FALLBACK_HBM_GBS, "fallback"
 
 
-DECODE_SOURCES = ("pa_decode.cu", "pa_decode_common.cuh", "pa_decode_fma.cuh", "pa_decode_mma.cuh", "pa_ptx.cuh")
-PREFILL_SOURCES = ("pa_prefill.cu", "pa_tcgen05.cuh", "pa_ptx.cuh")
+DECODE_SOURCES = ("pa_decode.cu", "pa_decode_persist.cuh", "pa_decode_common.cuh", "pa_decode_fma.cuh", "pa_decode_mma.cuh",
+                  "pa_launch.cuh", "pa_ptx.cuh")
+PREFILL_SOURCES = ("pa_prefill.cu", "pa_launch.cuh", "pa_tcgen05.cuh", "pa_ptx.cuh")
 
 
 def decode_source_hash(sources=None):
