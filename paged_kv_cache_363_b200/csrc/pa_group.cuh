@@ -78,21 +78,25 @@ inline int group_max_chunks(int64_t max_len, int64_t rows, int group, int num_kv
 // x tiles of 64 tokens), the longest table, and the (row, head) pairs.  Unsplit, the time is the longest table's or the mean
 // load's, at about 1 us a step; split into the mean load of a CTA (256 tokens at least), that load's and the
 // partial states' (written and read at 5 TB/s), and 4 us where a split brings a merge with it.
-// A chunk is long enough for the units to fit whole rounds of the CTAs, where the tiles are few enough to tell (each
-// ends in a part of a chunk, taken as 3/4): two rounds, where the states are joined anyway, so that the two CTAs of
-// an SM even out better, else one.  Halves of the mean load alone gave 608 units of
-// 155 rows on three documents of 23,000 to 32,000 tokens (32 query heads on 8) for 296 CTAs: 145 us, 125 fitted.
+// A chunk is long enough for the units to fit one round of the CTAs, where the tiles are few enough to tell (each ends
+// in a part of a chunk, taken as 3/4); or, where the states are joined anyway, two rounds, if those are the shorter at
+// three steps of overhead a unit.  155 rows on three documents of 23,000 to 32,000 tokens, 32 query heads on 8, the
+// whole call: 202 us with half the mean load (608 units for 296 CTAs), 197 fitted to two rounds, 183 to one; 12 rows on
+// each of 24 of 3,000: 85 fitted to two, 91 to one.
 // (Splitting every batch into two units per CTA cost 16 sequences x 64 rows x 1500 tokens 90 us, 60 unsplit.)
 __device__ __forceinline__ int plan_chunk(float steps, float tiles, int ctas, int longest, float pairs, int max_chunks, int D, bool merge_anyway)
 {
     const float load = steps / (float)ctas;
     const int least = (longest + max_chunks - 1) / max_chunks;
-    float fit = (merge_anyway ? 32.f : 64.f) * load;
-    for (int rounds = merge_anyway ? 2 : 1; rounds > 0; --rounds) {
+    float fit = 64.f * load, best = 3e38f;
+    for (int rounds = 1; rounds <= (merge_anyway ? 2 : 1); ++rounds) {
         const float units = (float)(rounds * ctas) - 0.75f * tiles;
-        if (units >= 0.5f * (float)(rounds * ctas)) {
-            fit = 64.f * steps / units;
-            if (fit >= 256.f) break;
+        if (units < 0.5f * (float)(rounds * ctas)) continue;
+        const float c = fmaxf(fmaxf(64.f * steps / units, (float)least), 256.f);
+        const float cost = (float)rounds * ((float)longest / ceilf((float)longest / c) * (1.f / 64.f) + 3.f);
+        if (cost < best) {
+            best = cost;
+            fit = c;
         }
     }
     const int c = (max(max((int)fminf(fit, 1e9f), least), 256) + 63) / 64 * 64;
