@@ -273,7 +273,8 @@ PA_API size_t pa_evict_workspace_size(int num_seqs, int num_kv_heads, int max_co
  *                    (pa_decode_scores) and the token's position, distinct within a head
  *   context_lens, keep_lens  [num_seqs] int32 (device).  A sequence with a negative one, or
  *                    a context past max_context_len or its table row, raises
- *                    PA_DEV_BAD_CONTEXT and is left as it is
+ *                    PA_DEV_BAD_CONTEXT and is left as it is.  So does a kv head whose
+ *                    scores or positions change while the call runs, where it notices
  *   max_context_len  host-side upper bound, at most 262144 (else PA_ERR_UNSUPPORTED) and
  *                    at most score_stride
  *   workspace        device scratch of pa_evict_workspace_size() bytes, 16-byte aligned;

@@ -26,6 +26,7 @@
 
 #include <cstdint>
 
+#include "pa_evict_select.h"
 #include "pa_internal.h"
 #include "pa_launch.cuh"
 #include "pa_ptx.cuh"
@@ -34,7 +35,7 @@ namespace pa {
 namespace {
 
 constexpr int kMoveThreads = 256;
-constexpr int kBins = 2048;
+constexpr int kBins = kEvictBins;
 constexpr int kCachedContext = 49152;  // keys (4 bytes) and two masks of a context in shared memory
 constexpr unsigned kFew = 256;         // keys of one bin that are compared with one another
 constexpr int kSmallContext = 4096;    // scores, positions, blocks and the move list as well
@@ -43,16 +44,6 @@ constexpr int kSmallContext = 4096;    // scores, positions, blocks and the move
 constexpr int kFromGlobal = 0;  // nowhere: read again in every pass
 constexpr int kKeysCached = 1;  // their keys in shared memory
 constexpr int kAllCached = 2;   // scores, positions and the move list too; the CTA may move the rows itself
-
-// Scores in an unsigned order: larger is better, -0 and +0 alike, NaN above +inf.  Recent tokens
-// (the key's largest value) come above all of them.
-__device__ __forceinline__ uint32_t score_key(float score)
-{
-    if (score != score) return 0xfffffffeu;
-    const uint32_t b = __float_as_uint(score + 0.f);
-    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-}
-constexpr uint32_t kRecentKey = 0xffffffffu;
 
 // Exclusive prefix sum of one value per thread over the CTA; *total receives the sum.
 template <int THREADS>
@@ -199,8 +190,10 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictArgs a
     };
     // the n-th largest key, `prefix`, and how many of its equals are among the n; the recent tokens lie above [lo, hi]
     unsigned prefix = kRecentKey, need = (unsigned)n;
-    for (bool first = true;; first = false) {
-        const int shift = max(0, 21 - __clz((int)(hi - lo)));
+    KeyRange range{lo, hi};
+    for (int pass = 0; pass < kEvictPasses; ++pass) {
+        const bool first = pass == 0;
+        const int shift = range.shift();
         unsigned seen = 0;  // recent tokens
         for (int i0 = tid; i0 < L; i0 += THREADS * 8) {
             uint32_t k[8];
@@ -208,7 +201,7 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictArgs a
             for (int j = 0; j < 8; ++j) k[j] = i0 + j * THREADS < L ? key(i0 + j * THREADS) : 0u;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                if (i0 + j * THREADS < L && k[j] >= lo && k[j] <= hi) atomicAdd(&s_hist[(k[j] - lo) >> shift], 1u);
+                if (i0 + j * THREADS < L && range.has(k[j])) atomicAdd(&s_hist[range.bin(k[j], shift)], 1u);
                 seen += k[j] == kRecentKey ? 1u : 0u;
             }
         }
@@ -237,7 +230,7 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictArgs a
             for (int j = 0; j < BPT; ++j) {
                 if (!found && need <= above + c[j]) {
                     found = true;
-                    s_prefix = lo + ((unsigned)(kBins - 1 - BPT * tid - j) << shift);
+                    s_prefix = range.first((unsigned)(kBins - 1 - BPT * tid - j), shift);
                     s_need = need - above;
                     s_count = c[j];
                 }
@@ -249,8 +242,7 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictArgs a
         need = s_need;
         const unsigned count = s_count;
         if (shift == 0) break;
-        hi = min(hi, prefix + ((1u << shift) - 1u));
-        lo = prefix;
+        range = range.narrow(prefix, shift);
         if (count > kFew) continue;
         // few left: each is compared with all
         for (int i0 = tid; i0 < L; i0 += THREADS * 8) {
@@ -259,7 +251,10 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictArgs a
             for (int j = 0; j < 8; ++j) k[j] = i0 + j * THREADS < L ? key(i0 + j * THREADS) : kRecentKey;
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (k[j] >= lo && k[j] <= hi) s_hist[atomicAdd(&s_few, 1u)] = k[j];
+                if (range.has(k[j])) {
+                    const unsigned at = atomicAdd(&s_few, 1u);
+                    if (at < kFew) s_hist[at] = k[j];
+                }
         }
         __syncthreads();
         if (tid < count) {
@@ -323,6 +318,15 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictArgs a
     // gaps before slot n (low half) and kept tokens behind it (high half): as many of each.  A word has one kind or
     // the other, but for the one that slot n is in, whose kept tokens are the first to move.
     rank = block_scan<THREADS>(cnt, s_warp, &total);
+    if ((unsigned)total != (unsigned)(total >> 32)) {
+        // not n tokens: scores or positions changed between the passes.  The lists below have room for as many gaps
+        // as movers alone.
+        if (tid == 0) {
+            if constexpr (!MOVE) a.counts[sh] = ~0u;
+            atomicOr(a.status, PA_DEV_BAD_CONTEXT);
+        }
+        return;
+    }
     for (int w = w0; w < w1; ++w) {
         const uint32_t kept = s_mask[w];
         const int below = n - w * 32;
