@@ -470,6 +470,8 @@ PA_API pa_status pa_swap_blocks(void* dst_k_cache, void* dst_v_cache, const void
  * it).  An unreferenced cached block stays in the tree until a block is needed and
  * the free queue is empty; then the one released longest ago among those with no
  * cached children is evicted and reused.  Every call that takes blocks can evict.
+ * While a sequence references a cached block, those above it stay in the tree, also
+ * the unreferenced ones (pa_alloc_make_private leaves such): they are not available.
  */
 typedef struct pa_allocator pa_allocator;
 
@@ -482,7 +484,7 @@ typedef struct {
     int64_t tokens;            /* sum of the sequences' token counts */
     int64_t waste_tokens;      /* unused slots in the sequences' last blocks */
     int64_t cached_blocks;     /* blocks in the prefix tree (referenced or not) */
-    int64_t cached_free;       /* unreferenced cached blocks (reusable by eviction) */
+    int64_t cached_free;       /* unreferenced cached blocks (reusable by eviction, once none below is referenced) */
     int64_t host_blocks;       /* blocks of the host tier (0 without one) */
     int64_t host_free;         /* free host blocks */
     int64_t swapped_seqs;      /* sequences swapped out to the host tier */

@@ -41,7 +41,8 @@ and hangs them under that path, and gives a partial last block a fresh private
 block.  A cached block whose count reaches zero stays in the tree, unreferenced.
 Blocks come from the free queue first; when it is empty, the unreferenced cached
 block released earliest among those with no child in the tree is removed from the
-tree and reused.
+tree and reused.  An unreferenced block with a referenced one anywhere below it can not
+be reached by such removals, and is not available.
 """
 import copy
 from collections import OrderedDict, deque
@@ -78,8 +79,18 @@ class OracleAllocator:
         table = self.tables[seq_id]
         return table[i // self.B] * self.B + i % self.B
 
+    def _evictable(self):
+        """The unreferenced cached blocks with no referenced block below them."""
+        held = set()
+        for blk in self.key_of:
+            if self.ref[blk] > 0:
+                while blk >= 0 and blk not in held:
+                    held.add(blk)
+                    blk = self.key_of[blk][0]
+        return set(self.key_of) - held
+
     def available(self):
-        return len(self.free) + len(self.unreferenced)
+        return len(self.free) + len(self._evictable())
 
     def _take(self):
         if self.free:
@@ -138,7 +149,7 @@ class OracleAllocator:
             hits.append(blk)
             parent = blk
         need = len(full) - len(hits) + (1 if n % B else 0)
-        if need > self.available() - sum(1 for b in hits if self.ref[b] == 0):
+        if need > self.available() - len(self._evictable() & set(hits)):
             raise OutOfBlocks()
         table = []
         for blk in hits:

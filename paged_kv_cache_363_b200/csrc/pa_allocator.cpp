@@ -28,7 +28,10 @@
 // block stays private (it will be written).  A cached block whose count drops to
 // zero is kept, unreferenced, for later prompts.  A block is taken from the free
 // queue first; when that is empty, the unreferenced cached block released longest
-// ago that has no cached children (a leaf) is evicted from the tree and reused.
+// ago that has no cached children (a leaf) is evicted from the tree and reused.  A
+// sequence that took private copies of its first blocks (pa_alloc_make_private) may
+// still hold cached blocks behind them: an unreferenced block above a referenced one
+// stays in the tree, and does not count as available until that one is let go.
 #include <algorithm>
 #include <cstdint>
 #include <cstring>
@@ -79,6 +82,8 @@ struct pa_allocator {
     std::unordered_map<std::vector<int32_t>, int32_t, KeyHash> tree;
     std::vector<std::vector<int32_t>> node_key;  // per block: its key (empty = not in the tree)
     std::vector<int32_t> nchild;                 // per block: cached children
+    std::vector<int32_t> nheld;                  // per block: those of them that are held (below)
+    int64_t evictable = 0;                       // cached blocks that are not held
     std::map<uint64_t, int32_t> lru;             // unreferenced cached blocks by release stamp
     std::map<uint64_t, int32_t> leaves;          // those of them with no cached child (the evictable ones)
     std::vector<uint64_t> stamp;                 // per block: its key in lru (and leaves)
@@ -94,6 +99,8 @@ struct pa_allocator {
     uint64_t epoch = 0;
     std::vector<uint64_t> blk_epoch;
     std::vector<int32_t> blk_dref;
+    std::vector<uint64_t> held_epoch;
+    std::vector<int32_t> held_left;        // beam step: held children that a block keeps
     std::vector<Seq*> batch_seq;
     std::vector<int32_t> touched;          // beam step: blocks whose count it changes
     std::vector<const Seq*> beam_par;      // beam step: each new beam's parent
@@ -106,7 +113,25 @@ struct pa_allocator {
     }
 
     bool cached(int32_t b) const { return !node_key[(size_t)b].empty(); }
-    int64_t available() const { return (int64_t)free_q.size() + (int64_t)lru.size(); }
+    int64_t available() const { return (int64_t)free_q.size() + evictable; }
+
+    // A cached block is held while it or any cached block below it is referenced: evictions, leaf by leaf, reach every
+    // block that is not held.  hold_above and release_above follow a change of b's own to the blocks above it.
+    int32_t parent(int32_t b) const { return node_key[(size_t)b][0]; }
+    void hold_above(int32_t b)
+    {
+        for (int32_t p = parent(b); p >= 0; p = parent(p)) {
+            if (nheld[(size_t)p]++ > 0 || ref[(size_t)p] > 0) break;
+            --evictable;
+        }
+    }
+    void release_above(int32_t b)
+    {
+        for (int32_t p = parent(b); p >= 0; p = parent(p)) {
+            if (--nheld[(size_t)p] > 0 || ref[(size_t)p] > 0) break;
+            ++evictable;
+        }
+    }
 
     int64_t slot_of(const Seq& q, int64_t i) const
     {
@@ -125,6 +150,7 @@ struct pa_allocator {
         node_key[(size_t)b].clear();
         lru.erase(stamp[(size_t)b]);
         leaves.erase(stamp[(size_t)b]);
+        --evictable;
         if (p >= 0 && --nchild[(size_t)p] == 0 && ref[(size_t)p] == 0) leaves.emplace(stamp[(size_t)p], p);
     }
 
@@ -149,6 +175,10 @@ struct pa_allocator {
         if (ref[(size_t)b]++ == 0) {
             lru.erase(stamp[(size_t)b]);
             leaves.erase(stamp[(size_t)b]);
+            if (nheld[(size_t)b] == 0) {  // (a block without references is a cached one)
+                --evictable;
+                hold_above(b);
+            }
         }
     }
 
@@ -159,6 +189,10 @@ struct pa_allocator {
             stamp[(size_t)b] = clock++;
             lru.emplace(stamp[(size_t)b], b);
             if (nchild[(size_t)b] == 0) leaves.emplace(stamp[(size_t)b], b);
+            if (nheld[(size_t)b] == 0) {
+                ++evictable;
+                release_above(b);
+            }
         } else {
             free_q.push_back(b);
         }
@@ -246,9 +280,12 @@ pa_allocator* pa_alloc_create(int num_blocks, int block_size, const int32_t* fre
     a->ref.assign((size_t)num_blocks, 0);
     a->node_key.assign((size_t)num_blocks, std::vector<int32_t>());
     a->nchild.assign((size_t)num_blocks, 0);
+    a->nheld.assign((size_t)num_blocks, 0);
     a->stamp.assign((size_t)num_blocks, 0);
     a->blk_epoch.assign((size_t)num_blocks, 0);
     a->blk_dref.assign((size_t)num_blocks, 0);
+    a->held_epoch.assign((size_t)num_blocks, 0);
+    a->held_left.assign((size_t)num_blocks, 0);
     if (free_order) {
         std::vector<char> seen((size_t)num_blocks, 0);
         for (int i = 0; i < num_blocks; ++i) {
@@ -325,18 +362,18 @@ pa_status pa_alloc_add_seq_cached(pa_allocator* a, int64_t seq_id, const int32_t
     std::vector<int32_t> key((size_t)B + 1);
     std::vector<int32_t> hits;
     int32_t parent = -1;
-    int64_t hits_unreferenced = 0;
+    int64_t hits_evictable = 0;
     for (int j = 0; j < nfull; ++j) {
         key[0] = parent;
         std::memcpy(key.data() + 1, token_ids + (size_t)j * B, (size_t)B * sizeof(int32_t));
         auto it = a->tree.find(key);
         if (it == a->tree.end()) break;
         hits.push_back(it->second);
-        hits_unreferenced += a->ref[(size_t)it->second] == 0 ? 1 : 0;
+        hits_evictable += a->ref[(size_t)it->second] == 0 && a->nheld[(size_t)it->second] == 0 ? 1 : 0;
         parent = it->second;
     }
     const int64_t need = (int64_t)(nfull - (int)hits.size()) + (num_tokens % B ? 1 : 0);
-    if (need > a->available() - hits_unreferenced) {
+    if (need > a->available() - hits_evictable) {
         pa::set_error("pa_alloc_add_seq_cached: out of blocks");
         return PA_ERR_OOM;
     }
@@ -353,6 +390,7 @@ pa_status pa_alloc_add_seq_cached(pa_allocator* a, int64_t seq_id, const int32_t
         a->tree.emplace(key, b);
         a->node_key[(size_t)b] = key;
         if (parent >= 0) a->nchild[(size_t)parent] += 1;
+        a->hold_above(b);
         q.table.push_back(b);
         parent = b;
     }
@@ -475,8 +513,22 @@ pa_status pa_alloc_beam_step(pa_allocator* a, const int64_t* beam_ids, int num_b
     for (int i = 0; i < num_beams; ++i)
         for (int32_t b : a->seqs.find(beam_ids[i])->second.table) delta(b) -= 1;
     int64_t released = 0;
-    for (int32_t b : touched)
-        if (a->ref[(size_t)b] > 0 && a->ref[(size_t)b] + a->blk_dref[(size_t)b] == 0) released += 1;
+    auto left = [&](int32_t b) { return a->ref[(size_t)b] + (a->blk_epoch[(size_t)b] == ep ? a->blk_dref[(size_t)b] : 0); };
+    for (int32_t b : touched) {
+        if (left(b) > 0) continue;
+        if (a->cached(b)) {
+            if (a->nheld[(size_t)b] > 0) continue;  // counted below, from the last held block under it
+            for (int32_t p = a->parent(b); p >= 0; p = a->parent(p)) {
+                if (a->held_epoch[(size_t)p] != ep) {
+                    a->held_epoch[(size_t)p] = ep;
+                    a->held_left[(size_t)p] = a->nheld[(size_t)p];
+                }
+                if (--a->held_left[(size_t)p] > 0 || left(p) > 0) break;
+                released += 1;
+            }
+        }
+        released += 1;
+    }
     int64_t need = 0;
     for (int j = 0; j < num_new; ++j) {
         const pa_allocator::Seq& p = *par[(size_t)j];
