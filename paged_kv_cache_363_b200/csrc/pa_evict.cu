@@ -514,10 +514,18 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
 
 }  // namespace
 
+// Dynamic shared memory of the selection for contexts of up to max_context tokens.
+static size_t evict_smem(int max_context)
+{
+    const size_t n = (size_t)max_context;
+    size_t bytes = (n + 31) / 32 * 8 + (max_context <= kCachedContext ? n * 4 : 0);
+    if (max_context <= kSmallContext) bytes += n * 8 + n / 2 * 4 + (n / 16 + 1) * 4;
+    return bytes;
+}
+
 cudaError_t launch_evict(const EvictArgs& a, int head_dim, int elt_bytes, cudaStream_t stream)
 {
     const int rows = a.num_seqs * a.num_kv_heads;
-    const int words = (a.max_context_len + 31) / 32;
     const int cpr = head_dim * elt_bytes / 16;
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -526,8 +534,6 @@ cudaError_t launch_evict(const EvictArgs& a, int head_dim, int elt_bytes, cudaSt
     // launch and the list's way through memory; fewer CTAs would leave the moving to too few SMs.
     const bool small = a.max_context_len <= kSmallContext, fused = small && rows >= sms;
     const bool cached = a.max_context_len <= kCachedContext;
-    size_t smem = (size_t)words * 8 + (cached ? (size_t)a.max_context_len * 4 : 0);
-    if (small) smem += (size_t)a.max_context_len * 8 + (size_t)(a.max_context_len / 2) * 4 + (size_t)(a.max_context_len / 16 + 1) * 4;
     auto kernel = cached ? evict_select_kernel<1024, kKeysCached, 0> : evict_select_kernel<1024, kFromGlobal, 0>;
     if (small) kernel = evict_select_kernel<256, kAllCached, 0>;
     if (fused) {
@@ -538,9 +544,12 @@ cudaError_t launch_evict(const EvictArgs& a, int head_dim, int elt_bytes, cudaSt
             default: return cudaErrorInvalidValue;
         }
     }
+    // the most that any call of this kernel needs, not this call's need: another thread's call may come between here
+    // and the launch
+    const size_t most = evict_smem(small ? kSmallContext : (cached ? kCachedContext : kMaxEvictContext));
     cudaError_t e;
-    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
-    kernel<<<rows, small ? 256 : 1024, smem, stream>>>(a);
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most)) != cudaSuccess) return e;
+    kernel<<<rows, small ? 256 : 1024, evict_smem(a.max_context_len), stream>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess || fused) return e;
     // enough CTAs to fill the device, but none with less than one step of the longest list
     const int steps = (a.move_stride + kMoveThreads / cpr - 1) / (kMoveThreads / cpr);
