@@ -161,6 +161,17 @@ def _launch(stream, *tensors):
     return (torch._C._cuda_getCurrentRawStream(cur) if stream is None else stream.cuda_stream), ptrs
 
 
+def _workspace(need, device, stream):
+    """A workspace for one call, from the memory of the stream that the call runs on: that stream's earlier work is
+    done with it, and it goes back there when the call returns, for what the stream runs after the call."""
+    import torch
+    if stream is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    own = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    with torch.cuda.stream(own):
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+
+
 # ---------------------------------------------------------------- device calls
 
 def pa_decode_partition_size(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len,
@@ -196,7 +207,7 @@ def pa_decode(out, q, k_cache, v_cache, block_tables, context_lens, max_context_
         raise TypeError("block_tables and context_lens must be int32")
     if workspace is None:
         need = pa_decode_workspace_size(S, Hq, Hkv, D, B, int(max_context_len), int(partition_size))
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _workspace(need, q.device, stream)
     ws_ptr, ws_bytes = _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size()
     st = lib.pa_decode(_dev_ptr(out, "out"), _dev_ptr(q, "q"), _dev_ptr(k_cache, "k_cache"),
                        _dev_ptr(v_cache, "v_cache"), _dev_ptr(block_tables, "block_tables"),
@@ -289,7 +300,7 @@ def pa_decode_shared(out, q, k_cache, v_cache, block_tables, context_lens, group
         raise TypeError("q, out and the caches must share a dtype")
     if workspace is None:
         need = pa_decode_shared_workspace_size(S, Hq, Hkv, D, B, int(max_context_len), int(max_shared_len), groups, n)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _workspace(need, q.device, stream)
     handle, (*ptrs, ws) = _launch(stream, out, q, k_cache, v_cache, block_tables, context_lens, group_rows, group_start,
                                   shared_lens, workspace)
     st = lib.pa_decode_shared(*ptrs, S, Hq, Hkv, D, B, block_tables.shape[1], NB, groups, n, int(max_context_len),
@@ -326,7 +337,7 @@ def pa_decode_scores(out, scores, q, k_cache, v_cache, block_tables, context_len
         raise TypeError("scores must be float32")
     if workspace is None:
         need = pa_decode_scores_workspace_size(S, Hq, Hkv, D, B, int(max_context_len), int(partition_size))
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _workspace(need, q.device, stream)
     handle, (*ptrs, ws) = _launch(stream, out, scores, q, k_cache, v_cache, block_tables, context_lens, workspace)
     st = lib.pa_decode_scores(*ptrs, S, Hq, Hkv, D, B, block_tables.shape[1], NB, int(max_context_len), scores.shape[2],
                               float(scale), int(partition_size), ws, workspace.numel() * workspace.element_size(),
@@ -360,7 +371,7 @@ def pa_evict(k_cache, v_cache, new_scores, new_positions, scores, positions, blo
         raise TypeError("the caches must share a dtype")
     if workspace is None:
         need = pa_evict_workspace_size(S, Hkv, int(max_context_len))
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=k_cache.device)
+        workspace = _workspace(need, k_cache.device, stream)
     handle, (*ptrs, ws) = _launch(stream, k_cache, v_cache, new_scores, new_positions, scores, positions, block_tables,
                                   context_lens, keep_lens, workspace)
     st = lib.pa_evict(*ptrs, int(num_recent), S, Hkv, D, B, block_tables.shape[1], NB, int(max_context_len),
@@ -474,7 +485,7 @@ def pa_cross_attention(out, q, k_cache, v_cache, block_tables, context_lens, q_s
         raise ValueError("lse must be float32 [Nq, Hq]")
     if workspace is None:
         need = pa_cross_attention_workspace_size(S, Hq, Hkv, D, B, Nq, int(max_query_len), int(max_context_len))
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _workspace(need, q.device, stream)
     handle, (*ptrs, ws) = _launch(stream, out, lse, q, k_cache, v_cache, block_tables, context_lens, q_start, workspace)
     st = lib.pa_cross_attention(*ptrs, S, Hq, Hkv, D, B, block_tables.shape[1], NB, Nq, int(max_query_len),
                                 int(max_context_len), float(scale), ws, workspace.numel() * workspace.element_size(),
