@@ -205,7 +205,8 @@ PA_API size_t pa_decode_shared_workspace_size(int num_seqs, int num_heads, int n
  *   shared_lens   [num_groups] int32 (device): tokens that the rows of group g share, whole
  *                 blocks, no more than any row's context.  The blocks are read through the
  *                 first row's table; that the other rows' tables begin with the same ones is
- *                 the caller's promise (pa_alloc_shared_groups finds such groups)
+ *                 the caller's promise (pa_alloc_nested_groups and pa_alloc_shared_groups
+ *                 find such groups)
  *   max_shared_len  host-side upper bound of shared_lens
  *   workspace     device scratch of pa_decode_shared_workspace_size() bytes, 16-byte
  *                 aligned; no initial contents.  Calls that share it must be ordered on one
@@ -555,14 +556,24 @@ PA_API pa_status pa_alloc_beam_step(pa_allocator* a, const int64_t* beam_ids, in
 
 /*
  * Groups of the listed resident sequences (a batch, row i = seq_ids[i], all different) that
- * share leading full blocks, for pa_decode_shared.  A row is in one group at most; of all
- * groupings by common leading blocks this one saves the most block reads,
- * sum over groups of (rows - 1) * shared blocks, with larger groups where two save the same.
- * rows_out[n] receives the groups' rows (ascending within a group, groups by their first
+ * share leading full blocks, for pa_decode_shared.  A row is in one group at most, and no
+ * block is among the shared ones of two groups: of the rows with a common prefix either all
+ * are one group, or those that share longer prefixes are, and the others are in none.  Of
+ * all such groupings this one saves the most block reads, sum over groups of (rows - 1) *
+ * shared blocks, with larger groups where two save the same.  rows_out[n] receives the groups' rows (ascending within a group, groups by their first
  * row), starts_out[n/2 + 1] and lens_out[n/2] the starts and the shared tokens (at most n/2
  * groups: each has two rows or more), *num_groups_out their number.
  */
 PA_API pa_status pa_alloc_shared_groups(const pa_allocator* a, const int64_t* seq_ids, int n, int32_t* rows_out,
+                                        int32_t* starts_out, int32_t* lens_out, int* num_groups_out);
+
+/*
+ * pa_alloc_shared_groups for prompts on a common stem: groups may nest, so that the rows left
+ * over by a longer prefix are a group of the shorter one (whose blocks the longer one's group
+ * reads again).  Of all groupings by common leading blocks this one saves the most block
+ * reads, and never fewer than pa_alloc_shared_groups.  Arguments and order as there.
+ */
+PA_API pa_status pa_alloc_nested_groups(const pa_allocator* a, const int64_t* seq_ids, int n, int32_t* rows_out,
                                         int32_t* starts_out, int32_t* lens_out, int* num_groups_out);
 
 /*

@@ -36,10 +36,12 @@
 #include <cstdint>
 #include <cstring>
 #include <deque>
+#include <iterator>
 #include <map>
 #include <new>
 #include <string>
 #include <unordered_map>
+#include <utility>
 #include <vector>
 
 #include "pa.h"
@@ -261,6 +263,110 @@ struct pa_allocator {
         return slot_of(q, i);
     }
 };
+
+namespace {
+
+// One row of a batch: its full blocks.
+struct BatchRow {
+    const int32_t* t;
+    int32_t len, row;
+};
+
+// Leading blocks that two rows share.
+int32_t common_blocks(const BatchRow& x, const BatchRow& y)
+{
+    const int32_t m = std::min(x.len, y.len);
+    int32_t k = 0;
+    while (k < m && x.t[k] == y.t[k]) ++k;
+    return k;
+}
+
+// The batch's rows sorted by table: those that share d leading blocks are neighbours whose common lengths are d or
+// more, the intervals of the common-length array, nested like the prefixes themselves.  False if a sequence is
+// unknown or swapped out.
+bool sorted_rows(const pa_allocator* a, const int64_t* seq_ids, int n, std::vector<BatchRow>& v)
+{
+    v.resize((size_t)n);
+    for (int i = 0; i < n; ++i) {
+        auto it = a->seqs.find(seq_ids[i]);
+        if (it == a->seqs.end() || it->second.on_host) return false;
+        v[(size_t)i] = BatchRow{it->second.table.data(), (int32_t)(it->second.tokens / a->block_size), i};
+    }
+    std::sort(v.begin(), v.end(), [](const BatchRow& x, const BatchRow& y) {
+        const int32_t k = common_blocks(x, y);
+        if (k < std::min(x.len, y.len)) return x.t[k] < y.t[k];
+        return x.len != y.len ? x.len < y.len : x.row < y.row;
+    });
+    return true;
+}
+
+// Groups as the calls return them: each a list of rows with the shared blocks behind them.
+void write_groups(std::vector<std::vector<int32_t>>& groups, int block_size, int32_t* rows_out, int32_t* starts_out,
+                  int32_t* lens_out, int* num_groups_out)
+{
+    for (auto& r : groups) std::sort(r.begin(), r.end() - 1);
+    std::sort(groups.begin(), groups.end());  // by first row
+    int at = 0, ng = 0;
+    starts_out[0] = 0;
+    for (const auto& r : groups) {
+        for (size_t k = 0; k + 1 < r.size(); ++k) rows_out[at++] = r[k];
+        lens_out[ng] = r.back() * block_size;
+        starts_out[++ng] = at;
+    }
+    *num_groups_out = ng;
+}
+
+// What the rows under a prefix save at best, as a function of t, the blocks of the nearest prefix above that has a
+// group (0: none): convex, rising, piecewise linear over whole numbers.  at0 + sum of s * max(0, t - b) over (b, s).
+struct Saving {
+    int64_t at0 = 0;
+    std::map<int64_t, int64_t> slope;  // b -> s
+    int64_t sum_s = 0, sum_sb = 0;     // of s, and of s * b
+
+    void add(int64_t b, int64_t s)
+    {
+        slope[b] += s;
+        sum_s += s;
+        sum_sb += s * b;
+    }
+    void drop(std::map<int64_t, int64_t>::iterator it)
+    {
+        sum_s -= it->second;
+        sum_sb -= it->second * it->first;
+        slope.erase(it);
+    }
+    // adds what another prefix's rows save, the shorter list into the longer
+    void join(Saving& o)
+    {
+        if (o.slope.size() > slope.size()) std::swap(*this, o);
+        at0 += o.at0;
+        for (const auto& x : o.slope) add(x.first, x.second);
+    }
+    // The prefix itself, of d blocks, may have a group too: it saves d per row below that has none nearer, but for the
+    // first.  Returns the largest t at which that saves more than no group, or -1.
+    int64_t open(int64_t d)
+    {
+        while (!slope.empty() && slope.rbegin()->first >= d) drop(std::prev(slope.end()));  // t is below d
+        const int64_t c = at0 + d * sum_s - sum_sb - d;
+        if (at0 >= c) return -1;
+        int64_t pos = 0, val = at0, s = 0;  // value and slope from pos on
+        while (!slope.empty() && val + s * (slope.begin()->first - pos) < c) {
+            const auto it = slope.begin();
+            val += s * (it->first - pos);
+            pos = it->first;
+            s += it->second;
+            drop(it);
+        }
+        const int64_t t = pos + (c - val + s - 1) / s - 1;  // val + s (t - pos) < c <= val + s (t + 1 - pos)
+        const int64_t over = val + s * (t + 1 - pos) - c;
+        at0 = c;
+        if (over > 0) add(t, over);
+        add(t + 1, s - over);
+        return t;
+    }
+};
+
+}  // namespace
 
 extern "C" {
 
@@ -579,27 +685,11 @@ pa_status pa_alloc_shared_groups(const pa_allocator* a, const int64_t* seq_ids, 
         pa::set_error("pa_alloc_shared_groups: bad argument");
         return PA_ERR_INVALID;
     }
-    struct Row {
-        const int32_t* t;  // full blocks
-        int32_t len, row;
-    };
-    std::vector<Row> v((size_t)n);
-    for (int i = 0; i < n; ++i) {
-        auto it = a->seqs.find(seq_ids[i]);
-        if (it == a->seqs.end() || it->second.on_host) {
-            pa::set_error("pa_alloc_shared_groups: unknown or swapped-out sequence");
-            return PA_ERR_INVALID;
-        }
-        v[(size_t)i] = Row{it->second.table.data(), (int32_t)(it->second.tokens / a->block_size), i};
+    std::vector<BatchRow> v;
+    if (!sorted_rows(a, seq_ids, n, v)) {
+        pa::set_error("pa_alloc_shared_groups: unknown or swapped-out sequence");
+        return PA_ERR_INVALID;
     }
-    // Sorted by table, the rows that share d leading blocks are neighbours whose common lengths are d or
-    // more: the intervals of the common-length array, nested like the prefixes themselves.
-    std::sort(v.begin(), v.end(), [](const Row& x, const Row& y) {
-        const int32_t m = std::min(x.len, y.len);
-        for (int32_t k = 0; k < m; ++k)
-            if (x.t[k] != y.t[k]) return x.t[k] < y.t[k];
-        return x.len != y.len ? x.len < y.len : x.row < y.row;
-    });
     struct Group {
         int left, right;  // rows v[left .. right]
         int32_t blocks;
@@ -613,12 +703,7 @@ pa_status pa_alloc_shared_groups(const pa_allocator* a, const int64_t* seq_ids, 
     std::vector<Group> chosen;
     std::vector<Open> open;
     for (int i = 1; i <= n; ++i) {
-        int32_t lcp = 0;
-        if (i < n) {
-            const Row &x = v[(size_t)i - 1], &y = v[(size_t)i];
-            const int32_t m = std::min(x.len, y.len);
-            while (lcp < m && x.t[lcp] == y.t[lcp]) ++lcp;
-        }
+        const int32_t lcp = i < n ? common_blocks(v[(size_t)i - 1], v[(size_t)i]) : 0;
         int left = i - 1;
         size_t first = chosen.size();
         int64_t saved = 0;
@@ -643,23 +728,91 @@ pa_status pa_alloc_shared_groups(const pa_allocator* a, const int64_t* seq_ids, 
                 open.push_back(Open{lcp, left, first, saved});
         }
     }
-    std::vector<std::vector<int32_t>> rows;
+    std::vector<std::vector<int32_t>> groups;
     for (const Group& g : chosen) {
         std::vector<int32_t> r;
         for (int k = g.left; k <= g.right; ++k) r.push_back(v[(size_t)k].row);
-        std::sort(r.begin(), r.end());
         r.push_back(g.blocks);
-        rows.push_back(std::move(r));
+        groups.push_back(std::move(r));
     }
-    std::sort(rows.begin(), rows.end());  // by first row
-    int at = 0, ng = 0;
-    starts_out[0] = 0;
-    for (const auto& r : rows) {
-        for (size_t k = 0; k + 1 < r.size(); ++k) rows_out[at++] = r[k];
-        lens_out[ng] = r.back() * a->block_size;
-        starts_out[++ng] = at;
+    write_groups(groups, a->block_size, rows_out, starts_out, lens_out, num_groups_out);
+    return PA_OK;
+}
+
+pa_status pa_alloc_nested_groups(const pa_allocator* a, const int64_t* seq_ids, int n, int32_t* rows_out,
+                                 int32_t* starts_out, int32_t* lens_out, int* num_groups_out)
+{
+    if (!a || n < 0 || !num_groups_out || !starts_out || (n > 0 && (!seq_ids || !rows_out || !lens_out))) {
+        pa::set_error("pa_alloc_nested_groups: bad argument");
+        return PA_ERR_INVALID;
     }
-    *num_groups_out = ng;
+    std::vector<BatchRow> v;
+    if (!sorted_rows(a, seq_ids, n, v)) {
+        pa::set_error("pa_alloc_nested_groups: unknown or swapped-out sequence");
+        return PA_ERR_INVALID;
+    }
+    // The prefixes that two rows or more share, each after all those inside it: their blocks, the prefix around them,
+    // and for every row the longest one it is in.
+    struct Prefix {
+        int64_t blocks;
+        int around;
+        int64_t open_below;  // a group of its own pays where the nearest one around has this many blocks or fewer
+    };
+    std::vector<Prefix> prefixes;
+    std::vector<int> longest((size_t)n, -1);
+    struct Open {
+        int32_t blocks;
+        std::vector<int> inside;  // prefixes
+        std::vector<int> rows;    // in none of those
+    };
+    std::vector<Open> open;
+    std::vector<Saving> saving;   // of each prefix, until the one around takes it over
+    for (int i = 0; i < n; ++i) {
+        const int32_t before = i > 0 ? common_blocks(v[(size_t)i - 1], v[(size_t)i]) : 0;
+        const int32_t after = i + 1 < n ? common_blocks(v[(size_t)i], v[(size_t)i + 1]) : 0;
+        if (after > (open.empty() ? 0 : open.back().blocks)) open.push_back(Open{after, {}, {}});
+        // (the row lies in the interval of the longer of its two common lengths, which is open)
+        if (std::max(before, after) > 0) open.back().rows.push_back(i);
+        while (!open.empty() && open.back().blocks > after) {
+            Open o = std::move(open.back());
+            open.pop_back();
+            const int id = (int)prefixes.size();
+            Saving f;
+            for (int p : o.inside) {
+                prefixes[(size_t)p].around = id;
+                f.join(saving[(size_t)p]);
+                saving[(size_t)p] = Saving();
+            }
+            if (!o.rows.empty()) f.add(0, (int64_t)o.rows.size());
+            for (int r : o.rows) longest[(size_t)r] = id;
+            prefixes.push_back(Prefix{o.blocks, -1, f.open(o.blocks)});
+            saving.push_back(std::move(f));
+            if (after > 0 && (open.empty() || open.back().blocks < after)) open.push_back(Open{after, {}, {}});
+            if (!open.empty()) open.back().inside.push_back(id);
+        }
+    }
+    // from the outside in: the nearest prefix with a group, for each prefix (itself, if it has one)
+    std::vector<int> group((size_t)prefixes.size(), -1);
+    std::vector<int> at((size_t)prefixes.size(), -1);
+    std::vector<std::vector<int32_t>> groups;
+    for (int p = (int)prefixes.size() - 1; p >= 0; --p) {
+        const int around = prefixes[(size_t)p].around;
+        const int g = around < 0 ? -1 : group[(size_t)around];
+        const bool own = (g < 0 ? 0 : prefixes[(size_t)g].blocks) <= prefixes[(size_t)p].open_below;
+        group[(size_t)p] = own ? p : g;
+    }
+    for (int i = 0; i < n; ++i) {
+        const int p = longest[(size_t)i] < 0 ? -1 : group[(size_t)longest[(size_t)i]];
+        if (p < 0) continue;
+        if (at[(size_t)p] < 0) {
+            at[(size_t)p] = (int)groups.size();
+            groups.emplace_back();
+        }
+        groups[(size_t)at[(size_t)p]].push_back(v[(size_t)i].row);
+    }
+    for (size_t p = 0; p < prefixes.size(); ++p)
+        if (at[p] >= 0) groups[(size_t)at[p]].push_back((int32_t)prefixes[p].blocks);
+    write_groups(groups, a->block_size, rows_out, starts_out, lens_out, num_groups_out);
     return PA_OK;
 }
 

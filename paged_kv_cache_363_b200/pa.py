@@ -67,6 +67,7 @@ SIGNATURES = [
     ("pa_alloc_append_slots", _int, [_vp, _vp, _int, _vp, _vp, ctypes.POINTER(_int)]),
     ("pa_alloc_beam_step", _int, [_vp, _vp, _int, _vp, _vp, _int, _vp, _vp, ctypes.POINTER(_int)]),
     ("pa_alloc_shared_groups", _int, [_vp, _vp, _int, _vp, _vp, _vp, ctypes.POINTER(_int)]),
+    ("pa_alloc_nested_groups", _int, [_vp, _vp, _int, _vp, _vp, _vp, ctypes.POINTER(_int)]),
     ("pa_alloc_make_private", _int, [_vp, _i64, _int, _vp, ctypes.POINTER(_int)]),
     ("pa_alloc_truncate", _int, [_vp, _i64, _int]),
     ("pa_alloc_free_seq", _int, [_vp, _i64]),
@@ -283,7 +284,7 @@ def pa_decode_shared(out, q, k_cache, v_cache, block_tables, context_lens, group
                      max_context_len, max_shared_len, scale, workspace=None, stream=None):
     """pa_decode of a batch in groups that share leading blocks, read once per group: group g has the batch rows
     group_rows[group_start[g]:group_start[g+1]] and shares shared_lens[g] tokens (whole blocks).  See
-    Allocator.shared_groups."""
+    Allocator.nested_groups."""
     import torch
     S, Hq, D = q.shape
     NB, Hkv, B, D2 = k_cache.shape
@@ -629,13 +630,20 @@ class Allocator:
 
     def shared_groups(self, seq_ids):
         """Groups of the batch's rows that share leading full blocks, for pa_decode_shared: (group_rows,
-        group_start, shared_lens) as int32 arrays."""
+        group_start, shared_lens) as int32 arrays.  No block is shared in two groups."""
+        return self._groups(lib.pa_alloc_shared_groups, "pa_alloc_shared_groups", seq_ids)
+
+    def nested_groups(self, seq_ids):
+        """shared_groups with groups that may nest, which saves the most block reads: rows that a longer prefix
+        leaves over are a group of the shorter one."""
+        return self._groups(lib.pa_alloc_nested_groups, "pa_alloc_nested_groups", seq_ids)
+
+    def _groups(self, call, name, seq_ids):
         ids = np.ascontiguousarray(seq_ids, dtype=np.int64)
         n = ids.shape[0]
         rows, starts, lens = np.empty(max(1, n), np.int32), np.empty(n // 2 + 1, np.int32), np.empty(n // 2 + 1, np.int32)
         ng = _int(0)
-        _check(lib.pa_alloc_shared_groups(self._h, _np_ptr(ids), n, _np_ptr(rows), _np_ptr(starts), _np_ptr(lens),
-                                          ctypes.byref(ng)), "pa_alloc_shared_groups")
+        _check(call(self._h, _np_ptr(ids), n, _np_ptr(rows), _np_ptr(starts), _np_ptr(lens), ctypes.byref(ng)), name)
         g = ng.value
         return rows[:starts[g]], starts[:g + 1], lens[:g]
 

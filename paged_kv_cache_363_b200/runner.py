@@ -33,7 +33,7 @@ class SharedDecode:
         """The allocator's groups for this step's rows, on the device: (rows, starts, shared lengths), and the
         longest shared length."""
         if getattr(self, "_groups", None) is None:
-            g = self.alloc.shared_groups(np.arange(self.wl.num_seqs, dtype=np.int64))
+            g = self.alloc.nested_groups(np.arange(self.wl.num_seqs, dtype=np.int64))
             self._groups = tuple(torch.from_numpy(x.copy()).to(self.device) for x in g), int(g[2].max(initial=0))
         return self._groups
 
