@@ -36,6 +36,7 @@
 #include <cstdint>
 #include <cstring>
 #include <deque>
+#include <exception>
 #include <iterator>
 #include <map>
 #include <new>
@@ -678,8 +679,8 @@ pa_status pa_alloc_beam_step(pa_allocator* a, const int64_t* beam_ids, int num_b
     return PA_OK;
 }
 
-pa_status pa_alloc_shared_groups(const pa_allocator* a, const int64_t* seq_ids, int n, int32_t* rows_out,
-                                 int32_t* starts_out, int32_t* lens_out, int* num_groups_out)
+static pa_status shared_groups(const pa_allocator* a, const int64_t* seq_ids, int n, int32_t* rows_out,
+                               int32_t* starts_out, int32_t* lens_out, int* num_groups_out)
 {
     if (!a || n < 0 || !num_groups_out || !starts_out || (n > 0 && (!seq_ids || !rows_out || !lens_out))) {
         pa::set_error("pa_alloc_shared_groups: bad argument");
@@ -739,8 +740,8 @@ pa_status pa_alloc_shared_groups(const pa_allocator* a, const int64_t* seq_ids, 
     return PA_OK;
 }
 
-pa_status pa_alloc_nested_groups(const pa_allocator* a, const int64_t* seq_ids, int n, int32_t* rows_out,
-                                 int32_t* starts_out, int32_t* lens_out, int* num_groups_out)
+static pa_status nested_groups(const pa_allocator* a, const int64_t* seq_ids, int n, int32_t* rows_out,
+                               int32_t* starts_out, int32_t* lens_out, int* num_groups_out)
 {
     if (!a || n < 0 || !num_groups_out || !starts_out || (n > 0 && (!seq_ids || !rows_out || !lens_out))) {
         pa::set_error("pa_alloc_nested_groups: bad argument");
@@ -814,6 +815,29 @@ pa_status pa_alloc_nested_groups(const pa_allocator* a, const int64_t* seq_ids, 
         if (at[p] >= 0) groups[(size_t)at[p]].push_back((int32_t)prefixes[p].blocks);
     write_groups(groups, a->block_size, rows_out, starts_out, lens_out, num_groups_out);
     return PA_OK;
+}
+
+// (the groups' lists grow with the batch: without the memory for them the call fails, and nothing leaves it)
+pa_status pa_alloc_shared_groups(const pa_allocator* a, const int64_t* seq_ids, int n, int32_t* rows_out,
+                                 int32_t* starts_out, int32_t* lens_out, int* num_groups_out)
+{
+    try {
+        return shared_groups(a, seq_ids, n, rows_out, starts_out, lens_out, num_groups_out);
+    } catch (const std::exception&) {
+        pa::set_error("pa_alloc_shared_groups: host allocation failed");
+        return PA_ERR_INVALID;
+    }
+}
+
+pa_status pa_alloc_nested_groups(const pa_allocator* a, const int64_t* seq_ids, int n, int32_t* rows_out,
+                                 int32_t* starts_out, int32_t* lens_out, int* num_groups_out)
+{
+    try {
+        return nested_groups(a, seq_ids, n, rows_out, starts_out, lens_out, num_groups_out);
+    } catch (const std::exception&) {
+        pa::set_error("pa_alloc_nested_groups: host allocation failed");
+        return PA_ERR_INVALID;
+    }
 }
 
 pa_status pa_alloc_make_private(pa_allocator* a, int64_t seq_id, int num_tokens, int64_t* pairs_out,

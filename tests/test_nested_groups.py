@@ -1,5 +1,8 @@
 """Groups of rows for pa_decode_shared that may nest (CPU only): against every way to group a small batch, and a recursion over
 the prefix tree for larger ones."""
+import os
+import subprocess
+import sys
 import time
 
 import numpy as np
@@ -154,3 +157,27 @@ def test_deep_nesting_in_time():
     saved, _ = _saved(a, np.arange(n), a.nested_groups)
     assert saved >= _saved(a, np.arange(n), a.shared_groups)[0] > 0
     assert len(lens) > 1
+
+
+@pytest.mark.parametrize("call", ["shared_groups", "nested_groups"])
+def test_without_host_memory_the_call_fails(call):
+    """A batch whose lists do not fit in the process's address space: an error, and the process lives on."""
+    program = """
+import resource
+import numpy as np
+from paged_kv_cache_363_b200 import pa
+a = pa.Allocator(4, 4)
+a.add_seq(0, 4)
+ids = np.zeros(60_000_000, np.int64)
+used = int(open("/proc/self/statm").read().split()[0]) * resource.getpagesize()
+resource.setrlimit(resource.RLIMIT_AS, (used + 900_000_000, used + 900_000_000))  # room for the 480 MB of results alone
+try:
+    a.%s(ids)
+except pa.PAError as e:
+    assert "host allocation failed" in str(e), e
+    print("refused")
+assert a.num_tokens(0) == 4
+""" % call
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", program], cwd=root, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and r.stdout.strip() == "refused", r.stderr
