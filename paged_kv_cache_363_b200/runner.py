@@ -30,26 +30,26 @@ class SharedDecode:
     """Decode of a batch whose sequences share leading blocks, each shared block read once per group."""
 
     def shared_groups(self):
-        """The allocator's groups for this step's rows, on the device: (rows, starts, shared lengths), and the
-        longest shared length."""
-        if getattr(self, "_groups", None) is None:
-            g = self.alloc.nested_groups(np.arange(self.wl.num_seqs, dtype=np.int64))
-            self._groups = tuple(torch.from_numpy(x.copy()).to(self.device) for x in g), int(g[2].max(initial=0))
-        return self._groups
+        """The allocator's groups of the batch's rows as they are now, on the device: (rows, starts, shared lengths),
+        and the longest shared length.  They go with the tables of the same moment."""
+        g = self.alloc.nested_groups(np.arange(self.wl.num_seqs, dtype=np.int64))
+        return tuple(torch.from_numpy(x.copy()).to(self.device) for x in g), int(g[2].max(initial=0))
 
-    def decode_shared(self, out=None, stream=None):
-        """The step's decode through pa_decode_shared (bf16)."""
+    def decode_shared(self, out=None, stream=None, groups=None):
+        """The step's decode through pa_decode_shared (bf16).  block_tables and context_lens are to be the allocator's
+        of now; `groups` (a result of shared_groups) for a step that is repeated or captured on the same ones."""
         out = self.out if out is None else out
         wl = self.wl
-        (rows, starts, lens), longest = self.shared_groups()
-        need = pa.pa_decode_shared_workspace_size(wl.num_seqs, wl.num_heads, wl.num_kv_heads, wl.head_dim,
-                                                  wl.block_size, self.max_context_len, longest, lens.shape[0],
-                                                  rows.shape[0])
-        if getattr(self, "shared_workspace", None) is None:
-            self.shared_workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=self.device)
+        with torch.cuda.stream(stream):      # (None: the current one)
+            (rows, starts, lens), longest = self.shared_groups() if groups is None else groups
+            need = pa.pa_decode_shared_workspace_size(wl.num_seqs, wl.num_heads, wl.num_kv_heads, wl.head_dim,
+                                                      wl.block_size, self.max_context_len, longest, lens.shape[0],
+                                                      rows.shape[0])
+            ws = getattr(self, "shared_workspace", None)
+            if ws is None or ws.numel() < need:
+                ws = self.shared_workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=self.device)
         return pa.pa_decode_shared(out, self.q, self.k_cache, self.v_cache, self.block_tables, self.context_lens, rows,
-                                   starts, lens, self.max_context_len, longest, wl.scale,
-                                   workspace=self.shared_workspace, stream=stream)
+                                   starts, lens, self.max_context_len, longest, wl.scale, workspace=ws, stream=stream)
 
 
 class DecodeBatch(SharedDecode):
