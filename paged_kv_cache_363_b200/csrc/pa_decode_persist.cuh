@@ -465,11 +465,15 @@ cudaError_t launch_persistent(const DecodeArgs& a, cudaStream_t stream)
     // b % Hkv of partition 0 of sequence b / Hkv without waiting for the plan.  The plan
     // grows an automatic partition only when the tokens of all sequences exceed
     // 4 x partition x CTAs, which the bound num_seqs x max_context_len rules out here.
+    // Only behind the call's own plan kernel, which itself starts when everything before it has finished: a run on an
+    // earlier plan may follow a kernel that lets its dependents start (another run, an unsplit pa_cross_attention, a
+    // pa_decode_scores in one launch) and whose output may be this run's q.
     args.planless = MODE == kModeScores && a.num_partitions == 1 && units <= ctas ? 1 : 0;
     const bool fixed_partition =
         !a.adaptive || (int64_t)a.num_seqs * a.max_context_len <= 4LL * args.partition_blocks * BS * (int64_t)grid;
     const int64_t pairs0 = (int64_t)a.num_seqs * a.num_kv_heads;
-    args.first_wave = fixed_partition || args.planless ? (int)(pairs0 < (int64_t)grid ? pairs0 : (int64_t)grid) : 0;
+    const bool behind_plan = (a.phases & kDecodePlan) != 0;
+    args.first_wave = (fixed_partition && behind_plan) || args.planless ? (int)(pairs0 < (int64_t)grid ? pairs0 : (int64_t)grid) : 0;
 
     if (a.was_planless) *a.was_planless = args.planless;
     if (args.planless) {
