@@ -197,7 +197,8 @@ PA_API size_t pa_decode_shared_workspace_size(int num_seqs, int num_heads, int n
  * pa_decode for a batch in groups whose sequences share their leading blocks (a system
  * prompt, the streams or beams of one prompt): the shared tokens are read once for all rows
  * of a group instead of once per row.  The result is pa_decode's up to rounding (the weights
- * of shared tokens are rounded to bf16 for their product with V).
+ * of shared tokens are rounded to bf16 for their product with V), but for NaN in q, K or V,
+ * which gives NaN in the rows and columns that see it.
  *   group_rows    [num_group_rows] int32 (device): the batch rows of the groups, each row
  *                 in one group at most; rows in no group attend on their own
  *   group_start   [num_groups + 1] int32 (device): group g has the rows
@@ -417,7 +418,9 @@ PA_API size_t pa_cross_attention_workspace_size(int num_seqs, int num_heads, int
  *   out[row][h] = sum_t softmax_t(scale * q[row][h] . K_t) V_t   over t < context_lens[s],
  * query head h reading kv head h / (num_heads / num_kv_heads).  A sequence may have no rows
  * (nothing is written) or no tokens (its rows become zero).  Sums and softmax are fp32; a
- * weight is rounded to bf16 for its product with V.
+ * weight is rounded to bf16 for its product with V, to a bf16 and a bf16 remainder where
+ * max_query_len is 1.  NaN in a query row or in a key it sees gives NaN in its out and lse,
+ * NaN in a value in that column.
  *   lse        [num_query_tokens][num_heads] fp32 (device, nullable): the natural logarithm
  *              of the sum of exp(scale * q . K_t), -inf without tokens
  *   q_start, context_lens  int32 (device), as for pa_prefill; a sequence whose rows leave

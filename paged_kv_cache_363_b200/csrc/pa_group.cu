@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                         *reinterpret_cast<float2*>(a.ws_ml + (o_row * a.num_partitions + it.chunk) * 2) =
                             make_float2(m_used, l);
                     } else if (a.lse) {
-                        a.lse[o_row] = (m_used + log2f(l)) * 0.6931471805599453f;
+                        a.lse[o_row] = row_lse(m_used, l);
                     }
                 }
             }
@@ -588,16 +588,14 @@ __global__ void __launch_bounds__(128) group_merge_kernel(const GroupArgs a)
             float wt = 0.f;  // lane i < 8: the weight of state c + i
             if (lane < CH && c + lane < np) {
                 const float2 v = __ldcg(ml + slot(c + lane));
-                wt = v.x == -INFINITY ? 0.f : exp2f(v.x - M);
+                wt = state_weight(v.x, v.y, M);
                 den = fmaf(wt, v.y, den);
             }
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
                 const float wi = __shfl_sync(0xffffffffu, wt, i);
-                if (wi != 0.f) {  // (a state without tokens has no values)
 #pragma unroll
-                    for (int k = 0; k < EPL; ++k) num[k] = fmaf(wi, x[i][k], num[k]);
-                }
+                for (int k = 0; k < EPL; ++k) num[k] = fmaf(wi, x[i][k], num[k]);
             }
         }
 #pragma unroll
@@ -612,7 +610,7 @@ __global__ void __launch_bounds__(128) group_merge_kernel(const GroupArgs a)
         } else {
             *reinterpret_cast<uint32_t*>(out) = pack_bf16(num[0] * inv, num[1] * inv);
         }
-        if (a.lse && lane == 0) a.lse[row] = den > 0.f ? (M + log2f(den)) * 0.6931471805599453f : -INFINITY;
+        if (a.lse && lane == 0) a.lse[row] = row_lse(M, den);
     }
 }
 

@@ -107,6 +107,18 @@ __device__ __forceinline__ int plan_chunk(float steps, float tiles, int ctas, in
     return whole <= parts ? longest : c;
 }
 
+// Weight of a partial state (m, l, O) in a join whose largest maximum is M.  NaN logits are no maximum, they show in
+// the sum alone: a state without a maximum weighs nothing, unless its sum is NaN.
+__device__ __forceinline__ float state_weight(float m, float l, float M)
+{
+    return m != -INFINITY ? exp2f(m - M) : (l == l ? 0.f : l);
+}
+// The natural log-sum-exp of a row: -inf without a sum, NaN where that is NaN.
+__device__ __forceinline__ float row_lse(float m, float l)
+{
+    return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
 // Entries go longest first, by sixteenths of the chunk: a CTA's units then are one of every length.
 constexpr int kLenClasses = 16;
 __device__ __forceinline__ int len_class(int kvlen, int chunk)

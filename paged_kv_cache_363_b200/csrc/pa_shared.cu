@@ -515,7 +515,7 @@ __device__ __forceinline__ void absorb_states(const SharedArgs& a, size_t row0, 
         }
 #pragma unroll
         for (int h = 0; h < (G >= 2 ? 2 : 1); ++h) {
-            const float w = valid ? exp2f(v[h].x - (h ? M1 : M0)) : 0.f;
+            const float w = valid ? state_weight(v[h].x, v[h].y, h ? M1 : M0) : 0.f;
             if (h) l1 = fmaf(w, v[h].y, l1);
             else l0 = fmaf(w, v[h].y, l0);
 #pragma unroll
@@ -600,7 +600,7 @@ __device__ __forceinline__ void write_row(const SharedArgs& a, size_t row0, OwnS
     constexpr int NV = D / 64;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     if (a.g.lse && t == 0 && g < G)
-        a.g.lse[row0 + g] = st.l > 0.f ? (st.m + log2f(st.l)) * 0.6931471805599453f : -INFINITY;
+        a.g.lse[row0 + g] = row_lse(st.m, st.l);
     st.scale(st.l > 0.f ? 1.f / st.l : 0.f, t);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
