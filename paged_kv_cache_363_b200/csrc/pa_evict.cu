@@ -553,7 +553,7 @@ cudaError_t launch_evict(const EvictArgs& a, int head_dim, int elt_bytes, cudaSt
     if ((e = cudaGetLastError()) != cudaSuccess || fused) return e;
     // enough CTAs to fill the device, but none with less than one step of the longest list
     const int steps = (a.move_stride + kMoveThreads / cpr - 1) / (kMoveThreads / cpr);
-    int splits = (148 * 16 + rows - 1) / rows;
+    int splits = (sms * 16 + rows - 1) / rows;
     splits = splits < steps ? splits : steps;
     splits = splits < 1 ? 1 : splits;
     const int carry = small ? 0 : (a.max_context_len + 8191) / 8192;
