@@ -751,7 +751,6 @@ pa_status pa_cross_attention(void* out, float* lse, const void* q, const void* k
     a.g.num_blocks = num_blocks;
     a.g.block_size = block_size;
     a.g.num_partitions = w.chunks;
-    a.g.lead_partitions = w.chunks;
     a.g.max_entries = (int)w.entries;
     a.g.max_merges = (int)w.merges;
     a.g.scale_log2 = scale * 1.4426950408889634f;
@@ -772,7 +771,6 @@ pa_status pa_cross_attention(void* out, float* lse, const void* q, const void* k
         o.num_seqs = num_seqs;
         o.max_context_len = max_context_len;
         o.max_parts = w.chunks;
-        o.g.lead_partitions = 0;
         e = launch_cross_single(o, q_start, num_query_tokens, head_dim, num_heads / num_kv_heads,
                                 static_cast<cudaStream_t>(stream));
     } else {

@@ -560,13 +560,12 @@ __global__ void __launch_bounds__(128) group_merge_kernel(const GroupArgs a)
     for (unsigned w = blockIdx.x * 4 + (threadIdx.x >> 5); w < total; w += gridDim.x * 4) {
         const uint2 e = __ldcg(a.merge_list + w / (unsigned)a.num_heads);
         const int h = (int)(w % (unsigned)a.num_heads);
-        const int nl = (int)(e.y & 0xffffu), np = nl + (int)(e.y >> 16);
+        const int np = (int)e.y;
         const size_t row = (size_t)e.x * a.num_heads + h;
         const float2* ml = reinterpret_cast<const float2*>(a.ws_ml) + row * a.num_partitions;
         const float* acc = a.ws_acc + row * a.num_partitions * D + lane * EPL;
-        auto slot = [&](int p) { return p < nl ? p : a.lead_partitions + p - nl; };
         float M = -INFINITY;
-        for (int p = lane; p < np; p += 32) M = fmaxf(M, __ldcg(ml + slot(p)).x);
+        for (int p = lane; p < np; p += 32) M = fmaxf(M, __ldcg(ml + p).x);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
         float num[EPL], den = 0.f;
@@ -576,7 +575,7 @@ __global__ void __launch_bounds__(128) group_merge_kernel(const GroupArgs a)
             float x[CH][EPL];
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
-                const float* src = acc + (size_t)slot(min(c + i, np - 1)) * D;
+                const float* src = acc + (size_t)min(c + i, np - 1) * D;
                 if constexpr (EPL == 4) {
                     const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
                     x[i][0] = v.x; x[i][1] = v.y; x[i][2] = v.z; x[i][3] = v.w;
@@ -587,7 +586,7 @@ __global__ void __launch_bounds__(128) group_merge_kernel(const GroupArgs a)
             }
             float wt = 0.f;  // lane i < 8: the weight of state c + i
             if (lane < CH && c + lane < np) {
-                const float2 v = __ldcg(ml + slot(c + lane));
+                const float2 v = __ldcg(ml + c + lane);
                 wt = state_weight(v.x, v.y, M);
                 den = fmaf(wt, v.y, den);
             }

@@ -29,7 +29,7 @@ struct GroupArgs {
     const int32_t* rows;          // query row of each member, or null
     const GroupItem* items;
     const unsigned* counts;       // [0] entries, [1] rows to merge
-    const uint2* merge_list;      // (row, first partial states | own partial states << 16)
+    const uint2* merge_list;      // (row, its partial states)
     float* ws_acc;                // [rows][num_heads][num_partitions][D]
     float* ws_ml;                 // [rows][num_heads][num_partitions][2]
     unsigned int* status;
@@ -39,7 +39,7 @@ struct GroupArgs {
     int num_blocks;
     int block_size;
     int num_partitions;           // partial states kept per (row, head)
-    int lead_partitions;          // of them, those of the tokens all members share (the others follow)
+    int lead_partitions;          // pa_decode_shared: of them, those of the shared tokens (the others follow)
     int max_entries;              // host bounds: entries, and rows to merge
     int max_merges;
     float scale_log2;
