@@ -60,7 +60,7 @@ constexpr int cmax(int a, int b) { return a > b ? a : b; }
 __device__ __forceinline__ int clamped_context(const DecodeArgs& a, int s, int block_size, bool flag)
 {
     int L = __ldg(a.context_lens + s);
-    const int Lcap = min(a.max_context_len, a.max_blocks_per_seq * block_size);
+    const int Lcap = min(a.max_context_len, table_tokens(a.max_blocks_per_seq, block_size));
     if (L < 0 || L > Lcap) {
         if (flag) atomicOr(a.status, PA_DEV_BAD_CONTEXT);
         L = L < 0 ? 0 : Lcap;

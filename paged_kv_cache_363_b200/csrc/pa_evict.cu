@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictArgs a
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int L = __ldg(a.context_lens + s), n = __ldg(a.keep_lens + s);
     if constexpr (!MOVE) pdl_launch_dependents();
-    if (L < 0 || n < 0 || L > a.max_context_len || L > a.max_blocks_per_seq * a.block_size) {
+    if (L < 0 || n < 0 || L > a.max_context_len || L > table_tokens(a.max_blocks_per_seq, a.block_size)) {
         if (tid == 0) {
             if constexpr (!MOVE) a.counts[sh] = ~0u;
             if (sh % a.num_kv_heads == 0) atomicOr(a.status, PA_DEV_BAD_CONTEXT);

@@ -625,7 +625,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) cross_plan_kernel(const Cross
     __shared__ int s_q0[kPlanThreads], s_n[kPlanThreads], s_len[kPlanThreads];
     pdl_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, S = a.num_seqs;
-    const int cap = min(a.max_context_len, (int)min((long long)a.g.max_blocks_per_seq * a.g.block_size, 0x7fffffffll));
+    const int cap = min(a.max_context_len, table_tokens(a.g.max_blocks_per_seq, a.g.block_size));
     const bool split = a.max_chunks > 1;
     if (tid < kLenClasses) s_class[tid] = 0;
     if (tid == 0) {

@@ -8,6 +8,12 @@
 namespace pa {
 namespace {
 
+// Tokens that a row of the block tables has room for, at most INT32_MAX: the product itself may be larger.
+__device__ __forceinline__ int table_tokens(int max_blocks_per_seq, int block_size)
+{
+    return (int)min((long long)max_blocks_per_seq * block_size, 0x7fffffffll);
+}
+
 // Launches a kernel with programmatic dependent launch: its CTAs may be scheduled
 // while the previous kernel in the stream drains; they wait (griddepcontrol.wait)
 // before touching that kernel's results.

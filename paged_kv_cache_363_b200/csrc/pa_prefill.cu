@@ -195,7 +195,7 @@ __device__ __forceinline__ bool item_geom(const PrefillArgs& a, int npairs, int 
     const int q1 = __ldg(a.q_start + it.s + 1);
     it.n = q1 - it.q0;
     it.L = __ldg(a.context_lens + it.s);
-    const int Lcap = a.max_blocks_per_seq * a.block_size;
+    const int Lcap = table_tokens(a.max_blocks_per_seq, a.block_size);
     it.bad = it.q0 < 0 || q1 > a.num_query_tokens || it.n < 0 || it.n > a.max_query_len || it.L > Lcap ||
              (CROSS ? it.L < 0 || it.L > a.max_context_len : it.L < it.n);
     it.t_lo0 = it.pair * kQT * T;

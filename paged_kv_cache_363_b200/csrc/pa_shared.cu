@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
         if (tid <= NG) s_start[tid] = g0;
         if (tid == 0 && NG == kPlanThreads) s_start[NG] = __ldg(a.group_start + NG);
     }
-    const int cap = min(a.max_context_len, (int)min((long long)a.g.max_blocks_per_seq * B, 0x7fffffffll));
+    const int cap = min(a.max_context_len, table_tokens(a.g.max_blocks_per_seq, B));
     for (int s = tid; s < S; s += kPlanThreads) {
         int L = __ldg(a.context_lens + s);
         if (L < 0 || L > cap) {
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     __shared__ unsigned s_own, s_big, s_front, s_back;
     pdl_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, S = a.num_seqs;
-    const int cap = min(a.max_context_len, (int)min((long long)a.g.max_blocks_per_seq * a.g.block_size, 0x7fffffffll));
+    const int cap = min(a.max_context_len, table_tokens(a.g.max_blocks_per_seq, a.g.block_size));
     if (tid == 0) s_own = s_big = s_front = s_back = 0;
     // row and tokens of sequence s; no row where its data is bad
     auto load = [&](int s, int& row, int& L, bool flag) {
