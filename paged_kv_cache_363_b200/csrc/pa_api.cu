@@ -686,7 +686,7 @@ size_t pa_cross_attention_workspace_size(int num_seqs, int num_heads, int num_kv
         check_group("pa_cross_attention_workspace_size", num_heads, num_kv_heads, 1, block_size, PA_DTYPE_BF16) != PA_OK)
         return 0;
     return cross_workspace((size_t)num_seqs, (size_t)num_heads, num_kv_heads, head_dim, (size_t)num_query_tokens,
-                           max_query_len, max_context_len)
+                           std::min(max_query_len, num_query_tokens), max_context_len)
         .total;
 }
 
@@ -708,6 +708,8 @@ pa_status pa_cross_attention(void* out, float* lse, const void* q, const void* k
         return PA_ERR_INVALID;
     }
     if (num_seqs == 0 || num_query_tokens == 0 || max_query_len == 0) return PA_OK;
+    // no sequence has more rows than there are; the bound chooses the kernel and counts its work items
+    max_query_len = std::min(max_query_len, num_query_tokens);
     if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !q_start) {
         set_error("pa_cross_attention: null pointer");
         return PA_ERR_INVALID;
