@@ -362,8 +362,8 @@ def pa_evict(k_cache, v_cache, new_scores, new_positions, scores, positions, blo
     shape = (S, Hkv, scores.shape[-1])
     if v_cache.shape != k_cache.shape or any(t.shape != shape for t in (scores, positions, new_scores, new_positions)):
         raise ValueError("shape mismatch: scores and positions are [S, Hkv, W]")
-    if block_tables.dim() != 2 or block_tables.shape[0] != S or keep_lens.shape != (S,):
-        raise ValueError("block_tables must be [S, max_blocks] and keep_lens [S]")
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,) or keep_lens.shape != (S,):
+        raise ValueError("block_tables must be [S, max_blocks], context_lens and keep_lens [S]")
     if scores.dtype != torch.float32 or new_scores.dtype != torch.float32:
         raise TypeError("scores must be float32")
     if any(t.dtype != torch.int32 for t in (positions, new_positions, block_tables, context_lens, keep_lens)):
@@ -476,8 +476,8 @@ def pa_cross_attention(out, q, k_cache, v_cache, block_tables, context_lens, q_s
     S = context_lens.shape[0]
     if D2 != D or v_cache.shape != k_cache.shape or out.shape != q.shape:
         raise ValueError("shape mismatch")
-    if block_tables.dim() != 2 or block_tables.shape[0] != S or q_start.shape != (S + 1,):
-        raise ValueError("block_tables must be [S, max_blocks] and q_start [S + 1]")
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,) or q_start.shape != (S + 1,):
+        raise ValueError("block_tables must be [S, max_blocks], context_lens [S] and q_start [S + 1]")
     if any(t.dtype != torch.int32 for t in (block_tables, context_lens, q_start)):
         raise TypeError("block_tables, context_lens and q_start must be int32")
     if not (out.dtype == q.dtype == k_cache.dtype == v_cache.dtype):
