@@ -186,7 +186,7 @@ pa_status decode_call(const char* fn, int phases, void* out, const void* q, cons
     }
     if (num_seqs == 0) return PA_OK;
     const bool run = (phases & kDecodeRun) != 0;
-    if ((run && (!out || !q || !k_cache || !v_cache)) || (with_scores && !scores) || !block_tables || !context_lens) {
+    if ((run && (!out || !q || !k_cache || !v_cache)) || (with_scores && !scores && max_context_len > 0) || !block_tables || !context_lens) {
         set_error(": null pointer");
         return PA_ERR_INVALID;
     }
@@ -710,7 +710,7 @@ pa_status pa_cross_attention(void* out, float* lse, const void* q, const void* k
     if (num_seqs == 0 || num_query_tokens == 0 || max_query_len == 0) return PA_OK;
     // no sequence has more rows than there are; the bound chooses the kernel and counts its work items
     max_query_len = std::min(max_query_len, num_query_tokens);
-    if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !q_start) {
+    if (!out || !q || !k_cache || !v_cache || (!block_tables && max_blocks_per_seq > 0) || !context_lens || !q_start) {
         set_error("pa_cross_attention: null pointer");
         return PA_ERR_INVALID;
     }
