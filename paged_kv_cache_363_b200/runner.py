@@ -29,11 +29,22 @@ def _round_up(x, m):
 class SharedDecode:
     """Decode of a batch whose sequences share leading blocks, each shared block read once per group."""
 
+    _last_groups = None     # on the host and on the device
+    _captured = ()          # what captured steps read, as long as the batch lives
+
     def shared_groups(self):
         """The allocator's groups of the batch's rows as they are now, on the device: (rows, starts, shared lengths),
-        and the longest shared length.  They go with the tables of the same moment."""
+        and the longest shared length.  They go with the tables of the same moment.  A stream that is being captured
+        cannot take them up: it gets those of the last call, as long as they are still the same."""
         g = self.alloc.nested_groups(np.arange(self.wl.num_seqs, dtype=np.int64))
-        return tuple(torch.from_numpy(x.copy()).to(self.device) for x in g), int(g[2].max(initial=0))
+        if torch.cuda.is_current_stream_capturing():
+            if self._last_groups is None or not all(np.array_equal(x, y) for x, y in zip(g, self._last_groups[0])):
+                raise ValueError("the groups are not on the device yet: call shared_groups before the capture")
+            return self._last_groups[1]
+        host = tuple(x.copy() for x in g)
+        dev = tuple(torch.from_numpy(x).to(self.device) for x in host), int(host[2].max(initial=0))
+        self._last_groups = host, dev
+        return dev
 
     def decode_shared(self, out=None, stream=None, groups=None):
         """The step's decode through pa_decode_shared (bf16).  block_tables and context_lens are to be the allocator's
@@ -48,6 +59,8 @@ class SharedDecode:
             ws = getattr(self, "shared_workspace", None)
             if ws is None or ws.numel() < need:
                 ws = self.shared_workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=self.device)
+            if torch.cuda.is_current_stream_capturing():
+                self._captured += ((rows, starts, lens, ws),)
         return pa.pa_decode_shared(out, self.q, self.k_cache, self.v_cache, self.block_tables, self.context_lens, rows,
                                    starts, lens, self.max_context_len, longest, wl.scale, workspace=ws, stream=stream)
 

@@ -80,3 +80,30 @@ def test_workspace_grows_with_the_batch_and_a_step_is_captured():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+def test_a_step_captured_after_a_call():
+    """Without `groups`: those of the call before, which the graph keeps; refused where they are not the batch's any more."""
+    from paged_kv_cache_363_b200 import pa
+    b = _batch()
+    want = b.decode_shared().clone()
+    torch.cuda.synchronize()
+    out = torch.empty_like(b.out)
+    g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(g, stream=side):
+        b.decode_shared(out=out, stream=side)
+    b.shared_workspace = None
+    for _ in range(3):                       # other calls, whose groups and workspace are their own
+        b.decode_shared(out=torch.empty_like(b.out))
+    junk = [torch.zeros(n, dtype=torch.uint8, device="cuda") for n in (64, 512, 512, 4096, 1 << 20)]
+    out.fill_(7.0)
+    g.replay()
+    torch.cuda.synchronize()
+    assert pa.pa_device_status() == 0
+    assert torch.equal(out, want) and len(junk) == 5
+    b = _batch()
+    with pytest.raises(ValueError):
+        with torch.cuda.graph(torch.cuda.CUDAGraph(), stream=side):
+            b.decode_shared(out=out, stream=side)
+    torch.cuda.synchronize()
+    _compare(pa, b)
